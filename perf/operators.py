@@ -293,7 +293,8 @@ def _plain_append(s):
     v = (vc * par[..., 1, :, :1] + par[..., 1, :, 1:]).reshape(*lead, D)
     k = torch.where(live, k, 0.0).to(_dtype(c))
     v = torch.where(live, v, 0.0).to(_dtype(c))
-    return {"k": k, "v": v, "key_inv": torch.where(live[..., 0], inv, 0.0)}
+    got = {"k": k, "v": v, "key_inv": torch.where(live[..., 0], inv, 0.0)}
+    return {**got, "tags": s["tags"][:-1]} if c["rounds"] else got
 
 
 def _softmax_attend(c, q, K, V, inv, admissible):
@@ -460,7 +461,7 @@ def _own(s):
                             buckets=s.get("new_buckets"), tags=s.get("tags"), **form)
         k, v, inv = lsh.lsh_cache_read(s["cache"], s["page_table"], s["ctx_len"], s["T"], c["D"],
                                        new_len=s["new_len"], out_dtype=_dtype(c), **form)
-        return {"k": k, "v": v, "key_inv": inv}
+        return {"k": k, "v": v, "key_inv": inv, **({"tags": s["tags"][:-1]} if c["rounds"] else {})}
     got, selected = {}, None
     if c["kind"] == "sparse":
         selected, scores = lsh.lsh_cache_select(s["tags"], s["q_buckets"], s["page_table"], s["ctx_len"],
