@@ -1,6 +1,6 @@
 /*
  * lsh_attention_hash.h -- C ABI of the B200 (sm_100a) shared-QK LSH attention
- * forward pass (the Reformer's LSH attention).
+ * (the Reformer's LSH attention): forward pass, backward, and decoding over a 4-bit cache.
  *
  * The method, as the pages state it:
  *   - Ultralytics glossary "Reformer", section "Atencao LSH": one shared
@@ -282,6 +282,139 @@ LSH_API lsh_status lsh_chunk_attend_backward(const void* qk, const void* v, int 
                                      int D, int n_rounds, const int32_t* perm, const int32_t* buckets,
                                      int chunk, int mask, float scale, const void* out, const float* lse,
                                      const void* dout, int out_dtype, float* dqk, float* dv, void* stream);
+
+/*
+ * ---- Decoding: a paged cache in 4 bits, attention over it, hash-selected pages ----
+ * The pages describe training; generating token by token needs the keys and values
+ * of every earlier position again at each step.  These calls keep them in 4 bits and
+ * attend to them, with the shared-QK conventions of lsh_chunk_attend (the query is the
+ * token's own qk row, keys are length-normalised, a token does not see itself unless
+ * it is its only key).
+ *
+ * The cache is one buffer [n_pages, H, block], block = lsh_cache_block_bytes(page, D,
+ * group) bytes.  A page holds `page` consecutive positions of one sequence (a power
+ * of two from 16 to 256); page_table [B, max_pages] names the physical page of each of
+ * a sequence's logical pages, in any order, and sequences may share pages that are only
+ * read.  Entries of logical pages that lie behind a sequence are not looked at.
+ *
+ * A stored value is z + s c with a code c of 0..15 and, per row and group of `group`
+ * dims, z = the largest bf16 not above the group's smallest value and s = the bf16 nearest to
+ * (largest - z) / 15; c = min(15, nearest integer to (x - z) / s, ties to even).  The
+ * quotients are the real numbers', so equal rows are stored equally by every kernel.
+ * A group whose s would be below 2^-100 is stored as z; a group that holds an infinity or a
+ * NaN, or whose range overflows a float, reads back as NaN.  Each K row also keeps
+ * 1 / max(||row||, 1e-12) of the row as it came, in fp32.  At D = 128 and group = 64 a
+ * token takes 148 bytes per head.
+ *
+ * Positions: ctx_len [B] int32 counts the tokens of each sequence in the cache, this
+ * call's among them.  Of the T rows of a call the first new_len[b] belong to sequence b
+ * (new_len null: all T) and are its last tokens: row i is position ctx_len[b] -
+ * new_len[b] + i.  Rows at or behind new_len[b], and rows whose position would be
+ * negative, are padding.  All three arrays are read on the device, so a captured graph
+ * replays with their current contents.
+ *
+ * Caller errors that only the device can see are recorded as LSH_ERR_INVALID_ARG in the
+ * device status word, and no access leaves a buffer: a ctx_len outside
+ * [0, max_pages * page] makes its sequence count as empty; a page id outside
+ * [0, n_pages) makes its page count as missing (not written, read back as zeros, not
+ * attended to); a bucket outside [0, 65536) is stored by its low 16 bits.
+ *
+ * Requires D of 64, 128 or 256 and group of 32 or 64 (LSH_ERR_UNSUPPORTED otherwise).
+ */
+
+/* Bytes of one (page, head) block of the cache, a multiple of 16; 0 for a form that no
+ * kernel serves. */
+LSH_API size_t lsh_cache_block_bytes(int page, int D, int group);
+
+/*
+ * lsh_cache_write -- quantise rows into the cache at their positions.
+ *
+ *   k, v       [B, H, T, D] dtype          in: key (shared qk) and value rows
+ *   buckets    [B, H, n_rounds, T] int32   in, nullable (with tags): lsh_hash's buckets
+ *   ctx_len, new_len, page_table           see above
+ *   cache      [n_pages, H, block]         in/out: only the rows' own bytes change
+ *   tags       [n_pages, H, n_rounds, page] 16-bit  in/out, nullable (with buckets): the
+ *              buckets by position, for lsh_cache_select; 1 <= n_rounds <= 64
+ *
+ * Two rows with the same place in one call (sequences that share a page they write to)
+ * leave that place with either row's bytes or a mixture.
+ */
+LSH_API lsh_status lsh_cache_write(const void* k, const void* v, int dtype, int B, int H, int T, int D,
+                                   const int32_t* buckets, int n_rounds, const int32_t* ctx_len,
+                                   const int32_t* new_len, const int32_t* page_table, int max_pages, int page,
+                                   int group, void* cache, int n_pages, uint16_t* tags, void* stream);
+
+/*
+ * lsh_cache_read -- the stored values of each sequence's last new_len[b] tokens (all of
+ * them with new_len = ctx_len), rounded once to out_dtype.
+ *
+ *   k, v       [B, H, T, D] out_dtype      out: K rows are not length-normalised; padding 0
+ *   key_inv    [B, H, T] float             out, nullable: 1 / length of the original K row;
+ *                                          padding 0
+ */
+LSH_API lsh_status lsh_cache_read(const void* cache, int n_pages, int B, int H, int T, int D,
+                                  const int32_t* ctx_len, const int32_t* new_len, const int32_t* page_table,
+                                  int max_pages, int page, int group, void* k, void* v, int out_dtype,
+                                  float* key_inv, void* stream);
+
+/*
+ * lsh_cache_select -- the pages each new token attends to, by shared buckets.
+ *
+ *   tags       [n_pages, H, n_rounds, page] 16-bit  in: from lsh_cache_write
+ *   q_buckets  [B, Hq, n_rounds, T] int32  in: buckets of the T rows' queries (lsh_hash);
+ *              Hq a multiple of H, query heads h Hq/H .. (h + 1) Hq/H - 1 use cached head h
+ *   mask       LSH_MASK_CAUSAL or 0: whether positions after the row's own count
+ *   scores     [B, H, T, max_pages] int32  out: per page the number of (query head of h,
+ *              round, admissible position) with equal buckets, the row's own position
+ *              included; -1 for pages without an admissible position
+ *   selected   [B, H, T, n_select] int32   out: the last n_local pages with an admissible
+ *              position and those of the highest scores, of equal scores the lowest pages;
+ *              n_select in all (or as many as there are), ascending, then -1
+ *
+ * 1 <= n_rounds <= 64, 0 <= n_local <= n_select; at most 128 query heads per cached head
+ * and 49152 logical pages (LSH_ERR_UNSUPPORTED beyond).
+ */
+LSH_API lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_buckets, int B, int Hq, int H,
+                                    int T, int n_rounds, const int32_t* ctx_len, const int32_t* new_len,
+                                    const int32_t* page_table, int max_pages, int page, int n_select, int n_local,
+                                    int mask, int32_t* selected, int32_t* scores, void* stream);
+
+/*
+ * Bytes of scratch that lsh_cache_attend needs for these sizes (0 when none); n_select 0
+ * without selection.
+ */
+LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, int D, int max_pages, int page,
+                                                int n_select);
+
+/*
+ * lsh_cache_attend -- attention of the T rows over their sequences' cached tokens, which
+ * include the rows themselves once lsh_cache_write has stored them.
+ *
+ *   q          [B, Hq, T, D] dtype         in: queries; Hq as for lsh_cache_select
+ *   selected   [B, H, T, n_select] int32   in, nullable (n_select 0 then): logical pages
+ *              that each row attends to, in any order; entries outside [0, max_pages) or
+ *              behind the sequence are skipped, a page listed twice counts twice
+ *   mask       LSH_MASK_SELF (a token does not see itself unless nothing else is
+ *              admissible to it) and LSH_MASK_CAUSAL (no later position); else 0
+ *   unit_keys  1: logits are divided by the key rows' original lengths (shared QK); 0: not
+ *   scale      logit scale; <= 0 selects 1/sqrt(D)
+ *   out        [B, Hq, T, D] out_dtype     out: softmax-weighted stored values; 0 for padding
+ *                                          and rows without an admissible key
+ *   lse        [B, Hq, T] float            out: log-sum-exp of the logits; -inf for those
+ *   workspace  device scratch of at least lsh_cache_attend_workspace_bytes(...) bytes,
+ *              contents undefined on entry and on exit; calls that may overlap on the GPU
+ *              (other streams, graphs replayed at the same time) need one each
+ *
+ * Sums are fp32.  bf16 queries enter the products exactly and the weights are rounded to
+ * bf16; fp32 queries and their weights enter as three bf16 pieces (24 bits).
+ * lse makes the result joinable with other key sets by lsh_combine_rounds.
+ */
+LSH_API lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int T, int D, const void* cache,
+                                    int n_pages, const int32_t* ctx_len, const int32_t* new_len,
+                                    const int32_t* page_table, int max_pages, int page, int group,
+                                    const int32_t* selected, int n_select, int mask, int unit_keys, float scale,
+                                    void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the current device's status

@@ -1,4 +1,4 @@
-"""B200-native shared-QK LSH attention (Reformer): forward pass and its backward.
+"""B200-native shared-QK LSH attention (Reformer): forward pass, its backward, and decoding over a 4-bit cache.
 
 The compute path lives in ``liblsh_attention_hash.so`` (hand-written sm_100a
 CUDA kernels behind a C ABI declared in ``include/lsh_attention_hash.h``).  This
@@ -20,6 +20,14 @@ from .binding import (  # noqa: F401
     lsh_get_device_status,
     lsh_attention,
     lsh_attention_host,
+    lsh_attention_decode,
+    alloc_cache,
+    lsh_cache_block_bytes,
+    lsh_cache_write,
+    lsh_cache_read,
+    lsh_cache_select,
+    lsh_cache_attend_workspace_bytes,
+    lsh_cache_attend,
     library_path,
     load_library,
 )

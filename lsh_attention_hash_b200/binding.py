@@ -49,6 +49,17 @@ _SIGS = {
                                     _c_int, _vp, _vp]),
     "lsh_chunk_attend_backward": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
                                            _c_int, _c_int, _c_float, _vp, _vp, _vp, _c_int, _vp, _vp, _vp]),
+    "lsh_cache_block_bytes": (_c_size, [_c_int] * 3),
+    "lsh_cache_write": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp,
+                                 _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp]),
+    "lsh_cache_read": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                                _vp, _vp, _c_int, _vp, _vp]),
+    "lsh_cache_select": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int,
+                                  _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "lsh_cache_attend_workspace_bytes": (_c_size, [_c_int] * 9),
+    "lsh_cache_attend": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _vp, _vp, _vp,
+                                  _c_int, _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _c_float, _vp, _c_int, _vp,
+                                  _vp, _c_size, _vp]),
     "lsh_get_device_status": (_c_int, [_vp]),
 }
 
@@ -293,6 +304,219 @@ def lsh_chunk_attend_backward(qk, v, perm, chunk, out, lse, dout, *, self_mask=T
     return dqk, dv
 
 
+def _on_device(dev, stream, tensors, call, where):
+    """Runs ``call(stream pointer)`` with ``dev`` current; every tensor must be on ``dev``."""
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{where}: all tensors must be on {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"{where}: the stream must be on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        _check(call(_stream(stream)), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(call(_stream(stream)), where)
+
+
+def lsh_cache_block_bytes(page, D, group):
+    """Bytes of one (page, head) block of the 4-bit cache (0 for a form that no kernel serves)."""
+    return int(load_library().lsh_cache_block_bytes(page, D, group))
+
+
+def alloc_cache(n_pages, H, D, *, page=64, group=64, n_rounds=0, device="cuda"):
+    """An empty 4-bit cache of ``n_pages`` pages: (cache, tags).
+
+    ``cache`` is uint8 [n_pages, H, block bytes]; ``tags`` (None with ``n_rounds`` 0) is int16
+    [n_pages, H, n_rounds, page], the 16-bit buckets by position that ``lsh_cache_select`` scores.
+    Nothing needs to be cleared: positions that were not written are not read.
+    """
+    block = lsh_cache_block_bytes(page, D, group)
+    if block == 0:
+        raise ValueError(f"no cache of page {page}, head dim {D}, group {group}")
+    cache = torch.empty((n_pages, H, block), dtype=torch.uint8, device=device)
+    tags = torch.empty((n_pages, H, n_rounds, page), dtype=torch.int16, device=device) if n_rounds else None
+    return cache, tags
+
+
+def _need_cache(cache, H, D, page, group):
+    _need(cache, "cache", torch.uint8)
+    block = lsh_cache_block_bytes(page, D, group)
+    if block == 0:
+        raise LSHError(8, f"no cache of page {page}, head dim {D}, group {group}")
+    if cache.dim() != 3 or cache.shape[1] != H or cache.shape[2] != block:
+        raise ValueError(f"cache must be [n_pages, {H}, {block}], got {tuple(cache.shape)}")
+    return cache.shape[0]
+
+
+def _need_lengths(page_table, ctx_len, new_len):
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    _need(ctx_len, "ctx_len", torch.int32, (B,))
+    if new_len is not None:
+        _need(new_len, "new_len", torch.int32, (B,))
+    return B, max_pages
+
+
+def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_len=None, buckets=None, tags=None,
+                    stream=None):
+    """Quantises rows ``k``, ``v`` [B,H,T,D] into the 4-bit ``cache`` at their positions.
+
+    ``ctx_len`` [B] int32 counts each sequence's cached tokens, these rows among them; the first
+    ``new_len[b]`` rows (default all T) are its last tokens, the others are padding.  With
+    ``buckets`` [B,H,n_rounds,T] (``lsh_hash``) and ``tags`` the rows' buckets are kept as well.
+    """
+    lib = load_library()
+    _need(k, "k")
+    if k.dim() != 4:
+        raise ValueError("k must be [B, H, T, D]")
+    B, H, T, D = k.shape
+    _need(v, "v", k.dtype, k.shape)
+    n_pages = _need_cache(cache, H, D, page, group)
+    Bt, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    if Bt != B:
+        raise ValueError(f"page_table has {Bt} sequences, k {B}")
+    n_rounds = 0
+    if buckets is not None or tags is not None:
+        if buckets is None or tags is None:
+            raise ValueError("buckets and tags go together")
+        _need(tags, "tags", torch.int16)
+        if tags.dim() != 4:
+            raise ValueError("tags must be [n_pages, H, n_rounds, page]")
+        n_rounds = tags.shape[2]
+        _need(tags, "tags", torch.int16, (n_pages, H, n_rounds, page))
+        _need(buckets, "buckets", torch.int32, (B, H, n_rounds, T))
+    _on_device(k.device, stream, (v, cache, page_table, ctx_len, new_len, buckets, tags),
+               lambda s: lib.lsh_cache_write(_ptr(k), _ptr(v), _dt(k), B, H, T, D, _ptr(buckets), n_rounds,
+                                             _ptr(ctx_len), _ptr(new_len), _ptr(page_table), max_pages, page, group,
+                                             _ptr(cache), n_pages, _ptr(tags), s), "lsh_cache_write")
+
+
+def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_len=None, out_dtype=torch.bfloat16,
+                   k=None, v=None, key_inv=None, stream=None):
+    """The stored values of each sequence's last ``new_len[b]`` (default T) tokens.
+
+    Returns (k, v [B,H,T,D] ``out_dtype``, key_inv [B,H,T] float32: 1 / length of the K rows as
+    they were written); padding rows are 0.  ``new_len=ctx_len`` reads whole sequences.
+    """
+    lib = load_library()
+    _need(cache, "cache", torch.uint8)
+    if cache.dim() != 3:
+        raise ValueError("cache must be [n_pages, H, block]")
+    H = cache.shape[1]
+    n_pages = _need_cache(cache, H, D, page, group)
+    B, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    if out_dtype not in _DT:
+        raise ValueError(f"unsupported dtype {out_dtype}")
+    dev = cache.device
+    k = torch.empty((B, H, T, D), dtype=out_dtype, device=dev) if k is None else _need(k, "k", out_dtype, (B, H, T, D))
+    v = torch.empty((B, H, T, D), dtype=out_dtype, device=dev) if v is None else _need(v, "v", out_dtype, (B, H, T, D))
+    if key_inv is None:
+        key_inv = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    _need(key_inv, "key_inv", torch.float32, (B, H, T))
+    _on_device(dev, stream, (page_table, ctx_len, new_len, k, v, key_inv),
+               lambda s: lib.lsh_cache_read(_ptr(cache), n_pages, B, H, T, D, _ptr(ctx_len), _ptr(new_len),
+                                            _ptr(page_table), max_pages, page, group, _ptr(k), _ptr(v),
+                                            _DT[out_dtype], _ptr(key_inv), s), "lsh_cache_read")
+    return k, v, key_inv
+
+
+def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=None, n_local=1, causal=True,
+                     selected=None, scores=None, stream=None):
+    """The ``n_select`` pages that each new token attends to: (selected, scores).
+
+    ``q_buckets`` [B,Hq,n_rounds,T] int32 are the new rows' buckets.  ``scores`` [B,H,T,max_pages]
+    int32 counts shared buckets (-1: no admissible position); ``selected`` [B,H,T,n_select] int32
+    lists the last ``n_local`` pages and those of the highest scores (ties: lowest page),
+    ascending, padded with -1.
+    """
+    lib = load_library()
+    _need(tags, "tags", torch.int16)
+    if tags.dim() != 4:
+        raise ValueError("tags must be [n_pages, H, n_rounds, page]")
+    n_pages, H, n_rounds, page = tags.shape
+    B, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    _need(q_buckets, "q_buckets", torch.int32)
+    if q_buckets.dim() != 4 or q_buckets.shape[0] != B or q_buckets.shape[2] != n_rounds:
+        raise ValueError(f"q_buckets must be [{B}, Hq, {n_rounds}, T]")
+    Hq, T = q_buckets.shape[1], q_buckets.shape[3]
+    dev = tags.device
+    if selected is None:
+        selected = torch.empty((B, H, T, n_select), dtype=torch.int32, device=dev)
+    if scores is None:
+        scores = torch.empty((B, H, T, max_pages), dtype=torch.int32, device=dev)
+    _need(selected, "selected", torch.int32, (B, H, T, n_select))
+    _need(scores, "scores", torch.int32, (B, H, T, max_pages))
+    _on_device(dev, stream, (q_buckets, page_table, ctx_len, new_len, selected, scores),
+               lambda s: lib.lsh_cache_select(_ptr(tags), n_pages, _ptr(q_buckets), B, Hq, H, T, n_rounds,
+                                              _ptr(ctx_len), _ptr(new_len), _ptr(page_table), max_pages, page,
+                                              n_select, n_local, 2 if causal else 0, _ptr(selected), _ptr(scores),
+                                              s), "lsh_cache_select")
+    return selected, scores
+
+
+def lsh_cache_attend_workspace_bytes(dtype, B, Hq, H, T, D, max_pages, page, n_select=0):
+    """Bytes of scratch that ``lsh_cache_attend`` needs for these sizes."""
+    return int(load_library().lsh_cache_attend_workspace_bytes(_DT[dtype], B, Hq, H, T, D, max_pages, page, n_select))
+
+
+def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_len=None, selected=None,
+                     self_mask=True, causal=True, unit_keys=True, scale=None, out_dtype=None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """Attention of the new rows' queries ``q`` [B,Hq,T,D] over their sequences' cached tokens.
+
+    Returns (out [B,Hq,T,D], lse [B,Hq,T] float32).  Hq is a multiple of the cache's H.
+    ``selected`` (``lsh_cache_select``) restricts each row to some pages.  ``self_mask``: a token
+    does not see itself unless nothing else is admissible; ``causal``: no later position;
+    ``unit_keys``: keys are length-normalised.  Rows without a key (padding) get 0 and -inf.
+    """
+    lib = load_library()
+    _need(q, "q")
+    _need(cache, "cache", torch.uint8)
+    if q.dim() != 4 or cache.dim() != 3:
+        raise ValueError("q must be [B, Hq, T, D] and cache [n_pages, H, block]")
+    B, Hq, T, D = q.shape
+    H = cache.shape[1]
+    n_pages = _need_cache(cache, H, D, page, group)
+    Bt, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    if Bt != B:
+        raise ValueError(f"page_table has {Bt} sequences, q {B}")
+    n_select = 0
+    if selected is not None:
+        _need(selected, "selected", torch.int32)
+        if selected.dim() != 4:
+            raise ValueError("selected must be [B, H, T, n_select]")
+        n_select = selected.shape[3]
+        _need(selected, "selected", torch.int32, (B, H, T, n_select))
+    out_dtype = q.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _DT:
+        raise ValueError(f"unsupported dtype {out_dtype}")
+    dev = q.device
+    if out is None:
+        out = torch.empty((B, Hq, T, D), dtype=out_dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    _need(out, "out", out_dtype, (B, Hq, T, D))
+    _need(lse, "lse", torch.float32, (B, Hq, T))
+    dt = _dt(q)
+    if workspace is None:
+        need = int(lib.lsh_cache_attend_workspace_bytes(dt, B, Hq, H, T, D, max_pages, page, n_select))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _need(workspace, "workspace", torch.uint8)
+    sc = 0.0 if scale is None else float(scale)
+    mask = (1 if self_mask else 0) | (2 if causal else 0)
+    _on_device(dev, stream, (cache, page_table, ctx_len, new_len, selected, out, lse, workspace),
+               lambda s: lib.lsh_cache_attend(_ptr(q), dt, B, Hq, H, T, D, _ptr(cache), n_pages, _ptr(ctx_len),
+                                              _ptr(new_len), _ptr(page_table), max_pages, page, group,
+                                              _ptr(selected), n_select, mask, 1 if unit_keys else 0, sc, _ptr(out),
+                                              _DT[out_dtype], _ptr(lse), _ptr(workspace),
+                                              workspace.numel() if workspace is not None else 0, s),
+               "lsh_cache_attend")
+    return out, lse
+
+
 def lsh_get_device_status(stream=None) -> int:
     """Synchronises the stream; returns and clears the device status word (0 = LSH_OK)."""
     return int(load_library().lsh_get_device_status(_stream(stream)))
@@ -327,6 +551,38 @@ def lsh_attention(qk, v, R, n_buckets, chunk, *, self_mask=True, causal=False, b
         return {"buckets": buckets, "near_tie": near, "perm": perm, "o_rounds": o, "lse_rounds": lse,
                 "out": out, "lse": lse_out}
     return out
+
+
+def lsh_attention_decode(qk, v, R, n_buckets, cache, tags, page_table, ctx_len, *, page=64, group=64, new_len=None,
+                         n_select=0, n_local=1, self_mask=True, scale=None, stream=None, bufs=None, check=False):
+    """One step of generation: the new tokens' rows join the cache and attend to it (causally).
+
+    ``qk``, ``v`` [B,H,T,D] are the new tokens' shared rows and values, ``ctx_len`` the sequences'
+    lengths with them.  The rows are hashed (with ``tags``) and written into the 4-bit cache; they then
+    attend to every earlier position (``n_select`` 0) or to the ``n_select`` pages in which
+    most cached tokens share their buckets.  Returns (out [B,H,T,D], lse [B,H,T]).
+
+    ``bufs`` may hold preallocated buffers (keys: buckets, selected, scores, out, lse, workspace).
+    ``check`` as for ``lsh_attention``.
+    """
+    b = bufs or {}
+    if n_select and tags is None:
+        raise ValueError("n_select needs tags")
+    buckets = None
+    if tags is not None:
+        buckets, _ = lsh_hash(qk, R, n_buckets, buckets=b.get("buckets"), with_near_tie=False, stream=stream)
+    lsh_cache_write(qk, v, cache, page_table, ctx_len, page=page, group=group, new_len=new_len, buckets=buckets,
+                    tags=tags, stream=stream)
+    selected = None
+    if n_select:
+        selected, _ = lsh_cache_select(tags, buckets, page_table, ctx_len, n_select, new_len=new_len, n_local=n_local,
+                                       selected=b.get("selected"), scores=b.get("scores"), stream=stream)
+    out, lse = lsh_cache_attend(qk, cache, page_table, ctx_len, page=page, group=group, new_len=new_len,
+                                selected=selected, self_mask=self_mask, scale=scale, out=b.get("out"),
+                                lse=b.get("lse"), workspace=b.get("workspace"), stream=stream)
+    if check:
+        _check(lsh_get_device_status(stream), "lsh_attention_decode (device status)")
+    return out, lse
 
 
 def lsh_attention_host(qk_h, v_h, R, n_buckets, chunk, out_h, *, groups=8, self_mask=True, causal=False,

@@ -1,0 +1,304 @@
+// C entry points of the 4-bit cache: argument checks, launch plans, dispatch.
+// Included at the end of lsh_api.cu (one translation unit).
+#pragma once
+
+#include "cache_attend.cuh"
+#include "cache_rw.cuh"
+#include "cache_select.cuh"
+
+namespace {
+
+// Form of a cache: what every entry point checks first.
+inline lsh_status check_cache_form(int H, int D, int page, int group, int n_pages, int B, int max_pages) {
+  if (B < 0 || H < 0 || n_pages < 0 || max_pages < 0) return LSH_ERR_SHAPE;
+  if (D < 8 || D > 256 || (D % 8) != 0) return LSH_ERR_SHAPE;
+  if (page < 16 || page > 256 || (page & (page - 1)) != 0) return LSH_ERR_SHAPE;
+  if (group < 8 || group > D || D % group != 0) return LSH_ERR_SHAPE;
+  if ((long long)max_pages * page > (1ll << 30)) return LSH_ERR_SHAPE;
+  if ((D != 64 && D != 128 && D != 256) || (group != 32 && group != 64)) return LSH_ERR_UNSUPPORTED;
+  return LSH_OK;
+}
+
+inline int log2_of(int p) {
+  int l = 0;
+  while ((1 << l) < p) ++l;
+  return l;
+}
+
+inline lsh::cache::Pages pages_of(const int32_t* table, const int32_t* ctx_len, const int32_t* new_len, int max_pages,
+                                  int page, int n_pages, int H, int T) {
+  lsh::cache::Pages p;
+  p.table = table;
+  p.ctx_len = ctx_len;
+  p.new_len = new_len;
+  p.max_pages = max_pages;
+  p.page_log2 = log2_of(page);
+  p.n_pages = n_pages;
+  p.H = H;
+  p.T = T;
+  return p;
+}
+
+// Calls f(integral_constant D, integral_constant GROUP) for a form check_cache_form accepts.
+template <typename Fn>
+lsh_status cache_form_dispatch(int D, int group, Fn f) {
+#define LSH_CF(DD, GG) \
+  if (D == DD && group == GG) return f(std::integral_constant<int, DD>(), std::integral_constant<int, GG>())
+  LSH_CF(64, 32);
+  LSH_CF(64, 64);
+  LSH_CF(128, 32);
+  LSH_CF(128, 64);
+  LSH_CF(256, 32);
+  LSH_CF(256, 64);
+#undef LSH_CF
+  return LSH_ERR_UNSUPPORTED;
+}
+
+// How an attention call is cut: query columns per cached head in tiles of 8 * nt, keys in splits.
+struct AttendPlan {
+  long long units;
+  int cols, nt, n_ct, split_tokens, n_splits;
+};
+
+inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int max_pages, int page, int n_select) {
+  AttendPlan p;
+  const bool sel = n_select > 0;
+  p.units = (long long)B * H * (sel ? T : 1);
+  p.cols = sel ? G : G * T;
+  p.nt = (dtype == LSH_BF16 && D <= 128 && p.cols > 8) ? 2 : 1;
+  p.n_ct = (p.cols + 8 * p.nt - 1) / (8 * p.nt);
+  const long long keys = (long long)(sel ? n_select : max_pages) * page;
+  const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
+  long long split = keys * p.units * p.n_ct / ((long long)sms * 12);
+  split = (split + 255) / 256 * 256;
+  split = std::min<long long>(std::max<long long>(split, 256), 4096);
+  p.split_tokens = (int)split;
+  p.n_splits = (int)std::max<long long>(1, (keys + split - 1) / split);
+  return p;
+}
+
+inline size_t attend_plan_bytes(const AttendPlan& p, int D) {
+  if (p.n_splits <= 1) return 0;
+  const size_t n = (size_t)p.units * p.n_splits * p.cols;
+  return n * D * sizeof(float) + (n * 2 * sizeof(float) + 15) / 16 * 16;
+}
+
+template <typename TQ, typename TO, int D, int GROUP, int NT>
+lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
+  using namespace lsh::cache;
+  using C = AttendCfg<TQ, D, GROUP, NT>;
+  auto kfn = cache_attend_kernel<TQ, TO, D, GROUP, NT>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+    return LSH_ERR_CUDA;
+  const long long grid = p.units * p.n_splits * p.n_ct;
+  kfn<<<(unsigned)grid, kAttThreads, C::kSmem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
+  if (p.n_splits == 1) return LSH_OK;
+  // the join may be set up while the last splits run; it waits for them before it reads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.units * p.cols));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<TO, D>, a) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lsh_cache_block_bytes(int page, int D, int group) {
+  if (check_cache_form(1, D, page, group, 1, 1, 1) != LSH_OK) return 0;
+  return (size_t)(page / 16) * lsh::cache::tile_bytes(D, group);
+}
+
+lsh_status lsh_cache_write(const void* k, const void* v, int dtype, int B, int H, int T, int D,
+                           const int32_t* buckets, int n_rounds, const int32_t* ctx_len, const int32_t* new_len,
+                           const int32_t* page_table, int max_pages, int page, int group, void* cache, int n_pages,
+                           uint16_t* tags, void* stream) {
+  if (!valid_dtype(dtype)) return LSH_ERR_DTYPE;
+  const lsh_status st = check_cache_form(H, D, page, group, n_pages, B, max_pages);
+  if (st != LSH_OK) return st;
+  if (T < 0 || (long long)B * H * T >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if ((buckets == nullptr) != (tags == nullptr)) return LSH_ERR_INVALID_ARG;
+  if (tags && (n_rounds < 1 || n_rounds > 64)) return LSH_ERR_SHAPE;
+  if (!k || !v || !ctx_len || !page_table || !cache) return LSH_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(ctx_len) || !aligned16(page_table) || !aligned16(cache) ||
+      (new_len && !aligned16(new_len)) || (tags && (!aligned16(tags) || !aligned16(buckets))))
+    return LSH_ERR_ALIGN;
+  lsh::cache::WriteArgs a;
+  a.k = k;
+  a.v = v;
+  a.buckets = buckets;
+  a.cache = static_cast<uint8_t*>(cache);
+  a.tags = tags;
+  a.rows = (long long)B * H * T;
+  a.n_rounds = n_rounds;
+  a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
+  if (a.rows == 0 || max_pages == 0) return LSH_OK;
+  cudaStream_t s = as_stream(stream);
+  return cache_form_dispatch(D, group, [&](auto DC, auto GC) {
+    constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
+    const long long threads = a.rows * (DD / 8);
+    const unsigned grid = (unsigned)((threads + lsh::cache::kRwThreads - 1) / lsh::cache::kRwThreads);
+    if (dtype == LSH_F32)
+      lsh::cache::cache_write_kernel<float, DD, GG><<<grid, lsh::cache::kRwThreads, 0, s>>>(a);
+    else
+      lsh::cache::cache_write_kernel<__nv_bfloat16, DD, GG><<<grid, lsh::cache::kRwThreads, 0, s>>>(a);
+    return launch_status();
+  });
+}
+
+lsh_status lsh_cache_read(const void* cache, int n_pages, int B, int H, int T, int D, const int32_t* ctx_len,
+                          const int32_t* new_len, const int32_t* page_table, int max_pages, int page, int group,
+                          void* k, void* v, int out_dtype, float* key_inv, void* stream) {
+  if (!valid_dtype(out_dtype)) return LSH_ERR_DTYPE;
+  const lsh_status st = check_cache_form(H, D, page, group, n_pages, B, max_pages);
+  if (st != LSH_OK) return st;
+  if (T < 0 || (long long)B * H * T >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if (!k || !v || !ctx_len || !page_table || !cache) return LSH_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(ctx_len) || !aligned16(page_table) || !aligned16(cache) ||
+      (new_len && !aligned16(new_len)) || (key_inv && !aligned16(key_inv)))
+    return LSH_ERR_ALIGN;
+  lsh::cache::ReadArgs a;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.k = k;
+  a.v = v;
+  a.inv = key_inv;
+  a.rows = (long long)B * H * T;
+  a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
+  if (a.rows == 0) return LSH_OK;
+  cudaStream_t s = as_stream(stream);
+  return cache_form_dispatch(D, group, [&](auto DC, auto GC) {
+    constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
+    const long long threads = a.rows * (DD / 8);
+    const unsigned grid = (unsigned)((threads + lsh::cache::kRwThreads - 1) / lsh::cache::kRwThreads);
+    if (out_dtype == LSH_F32)
+      lsh::cache::cache_read_kernel<float, DD, GG><<<grid, lsh::cache::kRwThreads, 0, s>>>(a);
+    else
+      lsh::cache::cache_read_kernel<__nv_bfloat16, DD, GG><<<grid, lsh::cache::kRwThreads, 0, s>>>(a);
+    return launch_status();
+  });
+}
+
+lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_buckets, int B, int Hq, int H, int T,
+                            int n_rounds, const int32_t* ctx_len, const int32_t* new_len, const int32_t* page_table,
+                            int max_pages, int page, int n_select, int n_local, int mask, int32_t* selected,
+                            int32_t* scores, void* stream) {
+  const lsh_status st = check_cache_form(H, 128, page, 64, n_pages, B, max_pages);
+  if (st != LSH_OK) return st;
+  if (T < 0 || Hq < 0 || (H == 0 ? Hq != 0 : (Hq % H != 0 || Hq == 0))) return LSH_ERR_SHAPE;
+  if (n_rounds < 1 || n_rounds > 64 || n_select < 1 || n_local < 0 || n_local > n_select) return LSH_ERR_SHAPE;
+  if ((long long)n_select * page > (1ll << 30)) return LSH_ERR_SHAPE;
+  if ((long long)B * H * T * std::max(1, n_select) >= (1ll << 31) ||
+      (long long)B * H * T * std::max(1, max_pages) >= (1ll << 31) || (long long)B * Hq * n_rounds * T >= (1ll << 31))
+    return LSH_ERR_SHAPE;
+  if (mask & ~LSH_MASK_CAUSAL) return LSH_ERR_INVALID_ARG;
+  if (!tags || !q_buckets || !ctx_len || !page_table || !selected || !scores) return LSH_ERR_INVALID_ARG;
+  if (!aligned16(tags) || !aligned16(q_buckets) || !aligned16(ctx_len) || !aligned16(page_table) ||
+      !aligned16(selected) || !aligned16(scores) || (new_len && !aligned16(new_len)))
+    return LSH_ERR_ALIGN;
+  const long long rows = (long long)B * H * T;
+  if (rows == 0) return LSH_OK;
+  // a lane's 16-bit counters and the scores of a row in shared memory
+  if (Hq / H > 128 || max_pages > lsh::cache::kMaxPickPages) return LSH_ERR_UNSUPPORTED;
+  lsh::cache::SelectArgs a;
+  a.tags = tags;
+  a.q_buckets = q_buckets;
+  a.scores = scores;
+  a.selected = selected;
+  a.B = B;
+  a.G = Hq / H;
+  a.n_rounds = n_rounds;
+  a.n_select = n_select;
+  a.n_local = n_local;
+  a.causal = (mask & LSH_MASK_CAUSAL) ? 1 : 0;
+  a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
+  cudaStream_t s = as_stream(stream);
+  const long long warps = (long long)B * H * max_pages;
+  const int per = lsh::cache::kScoreThreads / 32;
+  if (warps > 0) lsh::cache::cache_score_kernel<<<(unsigned)((warps + per - 1) / per), lsh::cache::kScoreThreads, 0, s>>>(a);
+  const int smem = max_pages > n_select ? max_pages * 4 : 16;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(lsh::cache::cache_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess)
+    return LSH_ERR_CUDA;
+  lsh::cache::cache_pick_kernel<<<(unsigned)rows, lsh::cache::kPickThreads, smem, s>>>(a);
+  return launch_status();
+}
+
+size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, int D, int max_pages, int page,
+                                        int n_select) {
+  if (!valid_dtype(dtype) || check_cache_form(H, D, page, 32, 1, B, max_pages) != LSH_OK) return 0;
+  if (H <= 0 || Hq <= 0 || Hq % H != 0 || T <= 0 || B <= 0 || n_select < 0) return 0;
+  return attend_plan_bytes(attend_plan(dtype, B, H, Hq / H, T, D, max_pages, page, n_select), D);
+}
+
+lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int T, int D, const void* cache,
+                            int n_pages, const int32_t* ctx_len, const int32_t* new_len, const int32_t* page_table,
+                            int max_pages, int page, int group, const int32_t* selected, int n_select, int mask,
+                            int unit_keys, float scale, void* out, int out_dtype, float* lse, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return LSH_ERR_DTYPE;
+  const lsh_status st = check_cache_form(H, D, page, group, n_pages, B, max_pages);
+  if (st != LSH_OK) return st;
+  if (T < 0 || Hq < 0 || (H == 0 ? Hq != 0 : (Hq % H != 0 || Hq == 0))) return LSH_ERR_SHAPE;
+  if ((long long)B * Hq * T >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if (selected ? n_select < 1 : n_select != 0) return LSH_ERR_INVALID_ARG;
+  if ((long long)n_select * page > (1ll << 30) || (long long)B * H * T * std::max(1, n_select) >= (1ll << 31))
+    return LSH_ERR_SHAPE;
+  if (mask & ~(LSH_MASK_SELF | LSH_MASK_CAUSAL)) return LSH_ERR_INVALID_ARG;
+  if (unit_keys != 0 && unit_keys != 1) return LSH_ERR_INVALID_ARG;
+  if (!q || !cache || !ctx_len || !page_table || !out || !lse) return LSH_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(ctx_len) || !aligned16(page_table) || !aligned16(out) ||
+      !aligned16(lse) || (new_len && !aligned16(new_len)) || (selected && !aligned16(selected)))
+    return LSH_ERR_ALIGN;
+  if ((long long)B * Hq * T == 0) return LSH_OK;
+  const AttendPlan p = attend_plan(dtype, B, H, Hq / H, T, D, max_pages, page, n_select);
+  if (p.units * p.n_splits * p.n_ct >= (1ll << 31)) return LSH_ERR_SHAPE;
+  const size_t need = attend_plan_bytes(p, D);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return LSH_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return LSH_ERR_ALIGN;
+  if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)D);
+  lsh::cache::AttendArgs a;
+  a.q = q;
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.selected = selected;
+  a.out = out;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = need ? a.part_o + (size_t)p.units * p.n_splits * p.cols * D : nullptr;
+  a.B = B;
+  a.G = Hq / H;
+  a.n_select = n_select;
+  a.causal = (mask & LSH_MASK_CAUSAL) ? 1 : 0;
+  a.self_mask = (mask & LSH_MASK_SELF) ? 1 : 0;
+  a.unit_keys = unit_keys;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.split_tokens = p.split_tokens;
+  a.n_splits = p.n_splits;
+  a.n_ct = p.n_ct;
+  a.cols = p.cols;
+  a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
+  cudaStream_t s = as_stream(stream);
+  return cache_form_dispatch(D, group, [&](auto DC, auto GC) -> lsh_status {
+    constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
+    using bf = __nv_bfloat16;
+    if (dtype == LSH_F32)
+      return out_dtype == LSH_F32 ? launch_cache_attend<float, float, DD, GG, 1>(a, p, s)
+                                  : launch_cache_attend<float, bf, DD, GG, 1>(a, p, s);
+    if constexpr (DD <= 128) {
+      if (p.nt == 2)
+        return out_dtype == LSH_F32 ? launch_cache_attend<bf, float, DD, GG, 2>(a, p, s)
+                                    : launch_cache_attend<bf, bf, DD, GG, 2>(a, p, s);
+    }
+    return out_dtype == LSH_F32 ? launch_cache_attend<bf, float, DD, GG, 1>(a, p, s)
+                                : launch_cache_attend<bf, bf, DD, GG, 1>(a, p, s);
+  });
+}
+
+}  // extern "C"

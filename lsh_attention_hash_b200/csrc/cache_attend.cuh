@@ -1,0 +1,697 @@
+// Attention of new tokens over the 4-bit cache: one pass with the running maximum
+// and sum of the softmax, split over the keys and joined by a second small kernel.
+//
+// With K = z + s c by groups of dims, a query's logit needs only whole codes on the
+// matrix units:  q . K = sum_grp ( s_grp sum_d q_d c_d + z_grp sum_d q_d ),  and
+// the output  O_d = sum_j (p_j s_j) c_jd + sum_j p_j z_j.  So codes 0..15 (exact in
+// bf16) are the A operand of mma.m16n8k16 and the queries (then the weights
+// p_j s_j) its B operand: S^T = K Q^T and O^T = V^T P^T, 8 query columns wide.  With
+// keys as the 16 rows no more than 8 columns are padded, and a group of query heads
+// or several new tokens share every key that is unpacked.
+//
+// A code becomes a bf16 by masking: 0x4300 | c is 128 + c.  For bf16 queries the 128 is
+// taken out on the other side: S starts at -128 sum q, and one more product per group
+// with a constant -128 operand gives O's share, so a code costs no arithmetic beyond
+// the mask.  fp32 queries are split into three bf16 pieces (24 bits) and the weights too;
+// there 128 is subtracted from the codes and the sums leave the matrix unit every
+// 32 tokens, so that its accumulation does not show.
+//
+// Every warp is a pipeline of its own: a lane copies 32 tokens (one or two
+// cp.async.bulk, codes and parameters together) into the warp's ring, kStages deep, and
+// the warp consumes them without a block barrier.  A split's warps meet once, at its end.
+// The maximum moves only when a logit exceeds it by 2^8: weights up to 256 cost nothing
+// in float, and the 32-lane maximum and the rescaling of O are left out of most steps.
+#pragma once
+
+#include "cache_common.cuh"
+#include "tc_common.cuh"
+
+namespace lsh {
+namespace cache {
+
+constexpr int kAttWarps = 4;
+constexpr int kAttThreads = kAttWarps * 32;
+constexpr int kStageTiles = 2;       // 32 tokens a copy
+constexpr int kStages = 3;           // copies in flight per warp
+constexpr int kMaxEntries = 512;     // pages of a split
+constexpr float kLazyMax = 8.f;
+
+struct AttendArgs {
+  const void* q;            // [B, H * G, T, D]
+  const uint8_t* cache;
+  const int32_t* selected;  // [B, H, T, n_select] or null
+  void* out;                // [B, H * G, T, D]
+  float* lse;               // [B, H * G, T]
+  float *part_o, *part_ml;  // [units, n_splits, cols, D], [units, n_splits, cols, 2]
+  int B, G, n_select;
+  int causal, self_mask, unit_keys;
+  float scale_log2;         // scale * log2(e)
+  int split_tokens, n_splits, n_ct, cols;
+  Pages pg;
+};
+
+// What a unit (a cached head of a sequence; with selection also one new token) attends to.
+struct Unit {
+  int b, h, t;        // t: the row with selection, else 0
+  int ctx, start;     // tokens in the cache, position of row 0
+  int n_new;
+  int n_list;         // tokens in list order: the positions themselves, or those of the selected pages
+};
+
+// Whether row t of the unit's sequence is one of its tokens (padding is answered with zeros).
+__device__ __forceinline__ bool row_live(const Unit& u, int t) { return t < u.n_new && u.start + t >= 0; }
+
+__device__ __forceinline__ Unit unit_of(const AttendArgs& a, int unit) {
+  Unit u;
+  const bool sel = a.selected != nullptr;
+  u.t = sel ? unit % a.pg.T : 0;
+  const int bh = sel ? unit / a.pg.T : unit;
+  u.b = bh / a.pg.H;
+  u.h = bh - u.b * a.pg.H;
+  u.ctx = ctx_of(a.pg, u.b);
+  u.n_new = new_of(a.pg, u.b);
+  u.start = u.ctx - u.n_new;
+  u.n_list = sel ? a.n_select << a.pg.page_log2 : u.ctx;
+  // no row with a position (the last row's is ctx - 1): nothing to do
+  if (sel ? !row_live(u, u.t) : !(u.n_new > 0 && u.ctx > 0)) u.n_list = 0;
+  return u;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two codes (the low nibbles of both halves of w >> 4 i) as bf16: 128 + c, or c with SUB.
+template <bool SUB>
+__device__ __forceinline__ uint32_t codes2(uint32_t w, int i) {
+  uint32_t x = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  if (SUB) {
+    const uint32_t c128 = 0x43004300u;
+    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&c128));
+    x = *reinterpret_cast<uint32_t*>(&r);
+  }
+  return x;
+}
+
+// N consecutive words of shared memory (8 or 16 byte loads).
+template <int N>
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p + 16 * i);
+      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+    }
+  }
+}
+
+template <typename TQ, int D, int GROUP, int NT>
+struct AttendCfg {
+  using F = Fmt<D, GROUP>;
+  static constexpr bool kF32 = sizeof(TQ) == 4;
+  static constexpr int kPieces = kF32 ? 3 : 1;
+  // 128 taken out of the codes: always in fp32; at D 256 the -128 products' accumulators would not fit
+  static constexpr bool kSub = kF32 || D == 256;
+  static constexpr int kKs = D / 16;  // k steps of Q K^T, m tiles of V^T P^T
+  static constexpr int kCols = 8 * NT;
+  static constexpr int kStageBytes = kStageTiles * F::kTile;
+  static constexpr int kRing = kAttWarps * kStages * kStageBytes;
+  static constexpr int kMerge = kAttWarps * kCols * D * 4;
+  static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
+  static constexpr int kOffQs = kOffQ + kPieces * NT * kKs * 32 * 8;
+  static constexpr int kOffMl = kOffQs + kCols * F::kGroups * 4;
+  static constexpr int kOffEnt = kOffMl + kAttWarps * kCols * 8;
+  static constexpr int kOffBar = kOffEnt + kMaxEntries * 8;
+  static constexpr int kSmem = kOffBar + kAttWarps * kStages * 8 + 16;
+  static constexpr int kRegQ = kPieces * NT * kKs * 2 <= 32;
+};
+
+template <typename TQ, typename TO, int D, int GROUP, int NT>
+__global__ void __launch_bounds__(kAttThreads)
+cache_attend_kernel(const __grid_constant__ AttendArgs a) {
+  using C = AttendCfg<TQ, D, GROUP, NT>;
+  using F = Fmt<D, GROUP>;
+  constexpr int NG = F::kGroups, KS = C::kKs, P = C::kPieces;
+  constexpr bool SUB = C::kSub;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int abort_flag;
+  uint2* qf = reinterpret_cast<uint2*>(smem + C::kOffQ);
+  float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  int2* ent = reinterpret_cast<int2*>(smem + C::kOffEnt);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int ct = blockIdx.x % a.n_ct;
+  const long long us = blockIdx.x / a.n_ct;
+  const int unit = (int)(us / a.n_splits), split = (int)(us - (long long)unit * a.n_splits);
+  const Unit u = unit_of(a, unit);
+  const bool sel = a.selected != nullptr;
+  const int col0 = ct * C::kCols;
+  const int list0 = split * a.split_tokens;
+  const int list1 = min(u.n_list, list0 + a.split_tokens);
+  if (list0 >= list1 && split > 0) return;  // the first split always answers, with nothing if there is nothing
+
+  // ---- set-up: page entries of the split, query fragments, barriers -------------------------------
+  const int pl = a.pg.page_log2;
+  const int32_t* picks = sel ? a.selected + ((long long)(u.b * a.pg.H + u.h) * a.pg.T + u.t) * a.n_select : nullptr;
+  const int e0 = list0 >> pl;
+  const int n_ent = list1 > list0 ? ((list1 - 1) >> pl) - e0 + 1 : 0;
+  for (int i = tid; i < n_ent; i += kAttThreads) {
+    int logical = e0 + i;
+    if (sel) logical = picks[e0 + i];
+    int phys = -1;
+    if (logical >= 0 && logical < a.pg.max_pages && ((long long)logical << pl) < u.ctx) phys = page_of(a.pg, u.b, logical);
+    ent[i] = make_int2(phys, logical << pl);
+  }
+  if (tid < kAttWarps * kStages) tc::mbar_init(bars + tid, 1);
+  if (tid == 0) abort_flag = 0;
+  auto q_row = [&](int col) -> const TQ* {  // the row of a column, or null
+    const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
+    return static_cast<const TQ*>(a.q) + (((long long)u.b * a.pg.H + u.h) * a.G + gg) * (long long)a.pg.T * D +
+           (long long)tt * D;
+  };
+  for (int i = tid; i < NT * KS * 32; i += kAttThreads) {
+    const int l = i & 31, ks = (i >> 5) % KS, nt = (i >> 5) / KS;
+    const int col = col0 + nt * 8 + (l >> 2);
+    const int d0 = 32 * (ks >> 1) + 8 * (ks & 1) + 2 * (l & 3);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (col < a.cols) {
+      const TQ* q = q_row(col);
+      x[0] = to_f32<TQ>(q[d0]); x[1] = to_f32<TQ>(q[d0 + 16]);
+      x[2] = to_f32<TQ>(q[d0 + 1]); x[3] = to_f32<TQ>(q[d0 + 17]);
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        y[k] = __bfloat162float(__float2bfloat16_rn(x[k]));
+        x[k] -= y[k];
+      }
+      qf[((p * NT + nt) * KS + ks) * 32 + l] = make_uint2(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]));
+    }
+  }
+  for (int i = tid; i < C::kCols * NG; i += kAttThreads) {
+    const int col = col0 + i / NG;
+    float s = 0.f;
+    if (col < a.cols) {
+      const TQ* q = q_row(col) + (i % NG) * GROUP;
+      for (int d = 0; d < GROUP; ++d) s += to_f32<TQ>(q[d]);
+    }
+    qs[i] = s;
+  }
+  tc::fence_mbar_init();
+  __syncthreads();
+
+  // ---- the lane's query columns (C fragment: columns 2 t4 and 2 t4 + 1 of each 8) ------------------
+  int pos[NT][2], last[NT][2];  // position; largest admissible position
+  bool self[NT][2];             // whether its own key is masked
+  int fast = u.ctx;             // tiles that end at or below are admissible to every column
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int col = col0 + nt * 8 + 2 * t4 + k;
+      const int tt = sel ? u.t : col / a.G;
+      const bool live = col < a.cols && row_live(u, tt);
+      pos[nt][k] = live ? u.start + tt : -1;
+      last[nt][k] = !live ? -1 : (a.causal ? pos[nt][k] : u.ctx - 1);
+      self[nt][k] = live && a.self_mask;
+      if (live && a.self_mask) {
+        // its own key counts when nothing else is admissible
+        bool other;
+        if (!sel) {
+          other = last[nt][k] > 0;
+        } else {
+          other = false;
+          for (int i = 0; i < a.n_select && !other; ++i) {
+            const int lp = picks[i];
+            if (lp < 0 || lp >= a.pg.max_pages) continue;
+            const long long f = (long long)lp << pl;
+            const long long e = min((long long)last[nt][k], f + (1 << pl) - 1);  // last admissible of the page
+            other = f <= e && (e > f || f != pos[nt][k]);
+          }
+        }
+        self[nt][k] = other;
+      }
+      if (live && (a.causal || a.self_mask)) fast = min(fast, pos[nt][k]);
+    }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) fast = min(fast, __shfl_xor_sync(0xffffffffu, fast, o));
+
+  uint2 qr[C::kRegQ ? P * NT * KS : 1];
+  if (C::kRegQ) {
+#pragma unroll
+    for (int i = 0; i < P * NT * KS; ++i) qr[i] = qf[i * 32 + lane];
+  }
+  auto qfrag = [&](int p, int nt, int ks) -> uint2 {
+    const int i = (p * NT + nt) * KS + ks;
+    return C::kRegQ ? qr[C::kRegQ ? i : 0] : qf[i * 32 + lane];
+  };
+  float qsum[NT][NG][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) qsum[nt][n][k] = qs[(nt * 8 + 2 * t4 + k) * NG + n];
+
+  float m[NT][2], l[NT][2];
+  float o[NT][KS][4], zs[NT][NG][2], cb[SUB ? 1 : NT][SUB ? 1 : NG][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      m[nt][k] = -INFINITY;
+      l[nt][k] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      zs[nt][n][0] = zs[nt][n][1] = 0.f;
+      if (!SUB)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cb[SUB ? 0 : nt][SUB ? 0 : n][k] = 0.f;
+    }
+  }
+
+  // ---- the warp's pipeline ------------------------------------------------------------------------
+  const int tile0 = list0 >> 4, tile1 = (list1 + 15) >> 4;  // tiles in list order
+  const int n_stage = list1 > list0 ? (tile1 - tile0 + kStageTiles - 1) / kStageTiles : 0;
+  uint8_t* ring = smem + warp * kStages * C::kStageBytes;
+  uint64_t* bar = bars + warp * kStages;
+  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st
+    uint32_t bytes = 0;
+    const uint8_t* src[kStageTiles];
+#pragma unroll
+    for (int k = 0; k < kStageTiles; ++k) {
+      const int tile = tile0 + st * kStageTiles + k;
+      src[k] = nullptr;
+      if (tile < tile1) {
+        const int2 e = ent[((tile << 4) >> pl) - e0];
+        const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
+        if (e.x >= 0 && p < u.ctx) {
+          src[k] = a.cache + tile_offset(a.pg, e.x, u.h, p, F::kTile);
+          bytes += F::kTile;
+        }
+      }
+    }
+    tc::mbar_arrive_expect_tx(bar + slot, bytes);
+    const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
+    if (src[0] && src[1] == src[0] + F::kTile) {
+      bulk_load(dst, src[0], kStageTiles * F::kTile, bar + slot);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kStageTiles; ++k)
+        if (src[k]) bulk_load(dst + k * F::kTile, src[k], F::kTile, bar + slot);
+    }
+  };
+  if (lane == 0)
+    for (int i = 0; i < kStages; ++i)
+      if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, i);
+
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int st = warp; st < n_stage; st += kAttWarps) {
+    if (!tc::mbar_wait(bar + slot, phase, &abort_flag)) {
+      // give the copies in flight the same time each, then leave
+      for (int i = 0, s2 = slot; i < kStages; ++i) {
+        if (st + i * kAttWarps < n_stage) {
+          const unsigned long long t0 = tc::globaltimer();
+          while (!tc::mbar_try_wait(bar + s2, (s2 < slot) ? phase ^ 1 : phase) && tc::globaltimer() - t0 < tc::kWaitNs) {
+          }
+        }
+        s2 = s2 + 1 == kStages ? 0 : s2 + 1;
+      }
+      break;
+    }
+    const uint8_t* buf = ring + slot * C::kStageBytes;
+    // ---- logits of 2 x 16 keys: s[..][nt][0,1]: key g, columns 2 t4, +1;  [2,3]: key g + 8
+    float s[kStageTiles][NT][4];
+    int first[kStageTiles];  // position of the tile's first token, or a value past every limit
+    bool any_tile = false;
+#pragma unroll
+    for (int k = 0; k < kStageTiles; ++k) {
+      const int tile = tile0 + st * kStageTiles + k;
+      first[k] = -1;
+      if (tile < tile1) {
+        const int2 e = ent[((tile << 4) >> pl) - e0];
+        const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
+        if (e.x >= 0 && p < u.ctx) first[k] = p;
+      }
+      any_tile |= first[k] >= 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[k][nt][c] = -INFINITY;
+      if (first[k] < 0) continue;
+      const uint8_t* tb = buf + k * F::kTile;
+      float acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
+      uint32_t wa[D / 32], wb[D / 32];
+      lds_words<D / 32>(tb + g * (D / 2) + t4 * (D / 8), wa);
+      lds_words<D / 32>(tb + (g + 8) * (D / 2) + t4 * (D / 8), wb);
+      const uint32_t* kp = reinterpret_cast<const uint32_t*>(tb + F::kOffKp);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        float part[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) part[nt][c] = SUB ? 0.f : -128.f * qsum[nt][n][c & 1];
+#pragma unroll
+        for (int kk = 0; kk < GROUP / 16; ++kk) {
+          const int ks = n * (GROUP / 16) + kk;
+          const int w = ks >> 1, i = (ks & 1) * 2;
+          const uint32_t a0 = codes2<SUB>(wa[w], i), a1 = codes2<SUB>(wb[w], i);
+          const uint32_t a2 = codes2<SUB>(wa[w], i + 1), a3 = codes2<SUB>(wb[w], i + 1);
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 b = qfrag(p, nt, ks);
+              mma16816(part[nt], a0, a1, a2, a3, b.x, b.y);
+            }
+        }
+        const uint32_t pa = kp[n * 16 + g], pb = kp[n * 16 + g + 8];
+        const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
+        const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            acc[nt][c] = fmaf(sa, part[nt][c], fmaf(za, qsum[nt][n][c], acc[nt][c]));
+            acc[nt][2 + c] = fmaf(sb, part[nt][2 + c], fmaf(zb, qsum[nt][n][c], acc[nt][2 + c]));
+          }
+      }
+      float fa = a.scale_log2, fb = a.scale_log2;
+      if (a.unit_keys) {
+        const float* inv = reinterpret_cast<const float*>(tb + F::kOffInv);
+        fa *= inv[g];
+        fb *= inv[g + 8];
+      }
+      const bool masked = first[k] + kTileTokens > fast;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x = acc[nt][c] * (c < 2 ? fa : fb);
+          if (masked) {
+            const int key = first[k] + g + (c < 2 ? 0 : 8);
+            if (key > last[nt][c & 1] || (key == pos[nt][c & 1] && self[nt][c & 1])) x = -INFINITY;
+          }
+          s[k][nt][c] = x;
+        }
+    }
+    if (any_tile) {
+      // ---- the running maximum, moved only when a logit is 2^8 above it
+      float top[NT][2];
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = s[0][nt][c];
+          x = fmaxf(x, s[0][nt][c + 2]);
+#pragma unroll
+          for (int k = 1; k < kStageTiles; ++k) x = fmaxf(fmaxf(x, s[k][nt][c]), s[k][nt][c + 2]);
+          top[nt][c] = x;
+          raise |= x > m[nt][c] + (m[nt][c] == -INFINITY ? 0.f : kLazyMax);
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = top[nt][c];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m[nt][c], x);
+            const float al = m[nt][c] == mn ? 1.f : exp2f(m[nt][c] - mn);
+            m[nt][c] = mn;
+            l[nt][c] *= al;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[nt][i][c] *= al;
+              o[nt][i][c + 2] *= al;
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+              zs[nt][n][c] *= al;
+              if (!SUB) {
+                cb[SUB ? 0 : nt][SUB ? 0 : n][c] *= al;
+                cb[SUB ? 0 : nt][SUB ? 0 : n][c + 2] *= al;
+              }
+            }
+          }
+      }
+      float fresh[P > 1 ? NT : 1][P > 1 ? KS : 1][4];  // fp32: this stage's sums
+      if (P > 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < kStageTiles; ++k) {
+        if (first[k] < 0) continue;
+        const uint8_t* tb = buf + k * F::kTile;
+        const bool masked = first[k] + kTileTokens > fast;
+        float p[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float base = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
+            p[nt][c] = P > 1 ? exp2f(s[k][nt][c] - base) : tc::ex2_approx(s[k][nt][c] - base);
+            l[nt][c & 1] += p[nt][c];
+          }
+        const uint32_t* vp = reinterpret_cast<const uint32_t*>(tb + F::kOffVp);
+        uint32_t pf[P][NG][NT][2];  // B fragments of (p s): [0] keys 0..7, [1] keys 8..15
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const uint32_t pa = vp[n * 16 + g], pb = vp[n * 16 + g + 8];
+          const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
+          const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4], z[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              w[c] = p[nt][c] * (c < 2 ? sa : sb);
+              z[c] = p[nt][c] * (c < 2 ? za : zb);
+              if (masked && s[k][nt][c] == -INFINITY) w[c] = z[c] = 0.f;  // whatever lies in a masked place
+            }
+            zs[nt][n][0] += z[0] + z[2];
+            zs[nt][n][1] += z[1] + z[3];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+              const uint32_t lo = tc::pack_bf16x2(w[0], w[1]), hi = tc::pack_bf16x2(w[2], w[3]);
+              pf[i][n][nt][0] = movmatrix(lo);
+              pf[i][n][nt][1] = movmatrix(hi);
+              if (i + 1 < P) {
+                w[0] -= bf16_bits(lo); w[1] -= __uint_as_float(lo & 0xffff0000u);
+                w[2] -= bf16_bits(hi); w[3] -= __uint_as_float(hi & 0xffff0000u);
+              }
+            }
+          }
+        }
+        const uint8_t* vrow = tb + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8);
+        uint32_t w0[D / 32], w1[D / 32];  // token pairs t4 and t4 + 4
+        lds_words<D / 32>(vrow, w0);
+        lds_words<D / 32>(vrow + 4 * D, w1);
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+          // the two tokens of a pair side by side: 16 dims in two words
+          uint32_t r0[2], r1[2];
+          r0[0] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x5410);
+          r0[1] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x7632);
+          r1[0] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x5410);
+          r1[1] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x7632);
+#pragma unroll
+          for (int mm = 0; mm < 4; ++mm) {
+            const int mt = 4 * q + mm, n = mt * 16 / GROUP, i = (mm & 1) * 2;
+            const uint32_t a0 = codes2<SUB>(r0[mm >> 1], i), a1 = codes2<SUB>(r0[mm >> 1], i + 1);
+            const uint32_t a2 = codes2<SUB>(r1[mm >> 1], i), a3 = codes2<SUB>(r1[mm >> 1], i + 1);
+#pragma unroll
+            for (int pc = P - 1; pc >= 0; --pc)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (P > 1)
+                  mma16816(fresh[P > 1 ? nt : 0][P > 1 ? mt : 0], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
+                else
+                  mma16816(o[nt][mt], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
+              }
+          }
+        }
+        if (!SUB) {
+          const uint32_t c = 0xc300c300u;  // -128 twice
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816(cb[SUB ? 0 : nt][SUB ? 0 : n], c, c, c, c, pf[0][n][nt][0], pf[0][n][nt][1]);
+        }
+      }
+      if (P > 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[nt][i][c] += fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c];
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && st + kStages * kAttWarps < n_stage) issue(st + kStages * kAttWarps, slot);
+    if (++slot == kStages) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+
+  // ---- join the warps -----------------------------------------------------------------------------
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) zs[nt][n][c] += __shfl_xor_sync(0xffffffffu, zs[nt][n][c], x);
+      }
+      if (g == 0) ml[warp * C::kCols + nt * 8 + 2 * t4 + c] = make_float2(m[nt][c], l[nt][c]);
+    }
+  __syncthreads();  // the ring is free
+  float* om = reinterpret_cast<float*>(smem);  // [warp][col][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const int n = i * 16 / GROUP;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float x = o[nt][i][c] + zs[nt][n][c & 1];
+        if (!SUB) x += cb[SUB ? 0 : nt][SUB ? 0 : n][c];
+        om[(warp * C::kCols + nt * 8 + 2 * t4 + (c & 1)) * D + i * 16 + g + (c < 2 ? 0 : 8)] = x;
+      }
+    }
+  __syncthreads();
+  for (int i = tid; i < C::kCols * D; i += kAttThreads) {
+    const int cc = i / D, d = i - cc * D, col = col0 + cc;
+    if (col >= a.cols) break;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) mx = fmaxf(mx, ml[w * C::kCols + cc].x);
+    float sum = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      const float2 v = ml[w * C::kCols + cc];
+      const float f = v.x == mx ? 1.f : exp2f(v.x - mx);
+      sum = fmaf(v.y, f, sum);
+      x = fmaf(om[(w * C::kCols + cc) * D + d], f, x);
+    }
+    if (a.n_splits == 1) {
+      const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
+      const long long row = (((long long)u.b * a.pg.H + u.h) * a.G + gg) * a.pg.T + tt;
+      if (!row_live(u, tt)) sum = 0.f;
+      static_cast<TO*>(a.out)[row * D + d] = from_f32<TO>(sum == 0.f ? 0.f : x / sum);
+      if (d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+    } else {
+      const long long pi = ((long long)unit * a.n_splits + split) * a.cols + col;
+      a.part_o[pi * D + d] = x;
+      if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pi) = make_float2(mx, sum);
+    }
+  }
+}
+
+// Joins the splits of a column: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+constexpr int kJoinThreads = 128;
+
+template <typename TO, int D>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;  // 4 dims a thread, the splits dealt out
+  __shared__ float4 so[kParts][kLanes];
+  __shared__ float2 sml[kParts];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int unit = blockIdx.x / a.cols, col = blockIdx.x - unit * a.cols;
+  const int j = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+  const Unit u = unit_of(a, unit);
+  const int n = u.n_list > 0 ? (u.n_list + a.split_tokens - 1) / a.split_tokens : 1;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (long long)unit * a.n_splits * a.cols + col;
+  const float* po = a.part_o + ((long long)unit * a.n_splits * a.cols + col) * D + 4 * j;
+  float mx = -INFINITY, sum = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = part; i < n; i += kParts) {
+    const float2 v = ml[(long long)i * a.cols];
+    const float4 y = *reinterpret_cast<const float4*>(po + (long long)i * a.cols * D);
+    const float mn = fmaxf(mx, v.x);
+    const float f = mx == mn ? 1.f : exp2f(mx - mn), e = v.x == mn ? 1.f : exp2f(v.x - mn);
+    mx = mn;
+    sum = sum * f + v.y * e;
+    x.x = x.x * f + y.x * e;
+    x.y = x.y * f + y.y * e;
+    x.z = x.z * f + y.z * e;
+    x.w = x.w * f + y.w * e;
+  }
+  so[part][j] = x;
+  if (j == 0) sml[part] = make_float2(mx, sum);
+  __syncthreads();
+  if (part) return;
+  float M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) M = fmaxf(M, sml[i].x);
+  sum = 0.f;
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kParts; ++i) {
+    const float f = sml[i].x == M ? 1.f : exp2f(sml[i].x - M);
+    sum = fmaf(sml[i].y, f, sum);
+    r[0] = fmaf(so[i][j].x, f, r[0]);
+    r[1] = fmaf(so[i][j].y, f, r[1]);
+    r[2] = fmaf(so[i][j].z, f, r[2]);
+    r[3] = fmaf(so[i][j].w, f, r[3]);
+  }
+  const bool sel = a.selected != nullptr;
+  const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
+  const long long row = (((long long)u.b * a.pg.H + u.h) * a.G + gg) * a.pg.T + tt;
+  if (!row_live(u, tt)) sum = 0.f;
+  TO* out = static_cast<TO*>(a.out) + row * D + 4 * j;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = from_f32<TO>(sum == 0.f ? 0.f : r[i] / sum);
+  if (j == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace cache
+}  // namespace lsh

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 #include <stdint.h>
 
 #include <cudaTypedefs.h>
@@ -701,3 +702,5 @@ lsh_status lsh_get_device_status(void* stream) {
 }
 
 }  // extern "C"
+
+#include "cache_api.cuh"
