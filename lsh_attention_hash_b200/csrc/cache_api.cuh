@@ -283,6 +283,8 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   a.n_splits = p.n_splits;
   a.n_ct = p.n_ct;
   a.cols = p.cols;
+  a.nibbles = 0x000f000fu;
+  a.c128 = 0x43004300u;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   cudaStream_t s = as_stream(stream);
   return cache_form_dispatch(D, group, [&](auto DC, auto GC) -> lsh_status {

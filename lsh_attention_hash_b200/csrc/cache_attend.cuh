@@ -23,6 +23,8 @@
 // in float, and the 32-lane maximum and the rescaling of O are left out of most steps.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_common.cuh"
 #include "tc_common.cuh"
 
@@ -47,6 +49,7 @@ struct AttendArgs {
   int causal, self_mask, unit_keys;
   float scale_log2;         // scale * log2(e)
   int split_tokens, n_splits, n_ct, cols;
+  uint32_t nibbles, c128;   // 0x000f000f, 0x43004300 (see codes2)
   Pages pg;
 };
 
@@ -97,12 +100,14 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   return y;
 }
 
-// Two codes (the low nibbles of both halves of w >> 4 i) as bf16: 128 + c, or c with SUB.
+// Two codes (the low nibbles of both halves of w >> 4 i) as bf16: 128 + c, or c with SUB.  The
+// constants come in as values (kernel arguments): as literals the mask and the exponent would be
+// two instructions, since one instruction holds one literal.
 template <bool SUB>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int i) {
-  uint32_t x = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t codes2(uint32_t w, int i, uint32_t nibbles, uint32_t c128) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w >> (4 * i)), "r"(nibbles), "r"(c128));  // (w & n) | c
   if (SUB) {
-    const uint32_t c128 = 0x43004300u;
     __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&c128));
     x = *reinterpret_cast<uint32_t*>(&r);
   }
@@ -141,7 +146,8 @@ struct AttendCfg {
   static constexpr int kOffMl = kOffQs + kCols * F::kGroups * 4;
   static constexpr int kOffEnt = kOffMl + kAttWarps * kCols * 8;
   static constexpr int kOffBar = kOffEnt + kMaxEntries * 8;
-  static constexpr int kSmem = kOffBar + kAttWarps * kStages * 8 + 16;
+  static constexpr int kOffDesc = kOffBar + kAttWarps * kStages * 8;
+  static constexpr int kSmem = kOffDesc + kAttWarps * kStages * 8;
   static constexpr int kRegQ = kPieces * NT * kKs * 2 <= 32;
 };
 
@@ -159,6 +165,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   int2* ent = reinterpret_cast<int2*>(smem + C::kOffEnt);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  int2* descs = reinterpret_cast<int2*>(smem + C::kOffDesc);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int ct = blockIdx.x % a.n_ct;
@@ -211,14 +218,19 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       qf[((p * NT + nt) * KS + ks) * 32 + l] = make_uint2(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]));
     }
   }
-  for (int i = tid; i < C::kCols * NG; i += kAttThreads) {
-    const int col = col0 + i / NG;
-    float s = 0.f;
-    if (col < a.cols) {
-      const TQ* q = q_row(col) + (i % NG) * GROUP;
-      for (int d = 0; d < GROUP; ++d) s += to_f32<TQ>(q[d]);
+  // sums of the queries by group: 16 threads a column, D/16 dims each
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int cc = nt * 8 + (tid >> 4), j = tid & 15;
+    float x = 0.f;
+    if (col0 + cc < a.cols) {
+      const TQ* q = q_row(col0 + cc) + j * (D / 16);
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) x += to_f32<TQ>(q[d]);
     }
-    qs[i] = s;
+#pragma unroll
+    for (int o = 1; o < 16 / NG; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (j % (16 / NG) == 0) qs[cc * NG + j / (16 / NG)] = x;
   }
   tc::fence_mbar_init();
   __syncthreads();
@@ -276,14 +288,14 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) qsum[nt][n][k] = qs[(nt * 8 + 2 * t4 + k) * NG + n];
 
-  float m[NT][2], l[NT][2];
+  float m[NT][2], base[NT][2], bar_m[NT][2], l[NT][2];  // maximum; what is subtracted; where it has to move
   float o[NT][KS][4], zs[NT][NG][2], cb[SUB ? 1 : NT][SUB ? 1 : NG][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      m[nt][k] = -INFINITY;
-      l[nt][k] = 0.f;
+      m[nt][k] = bar_m[nt][k] = -INFINITY;
+      base[nt][k] = l[nt][k] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < KS; ++i)
@@ -303,22 +315,28 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   const int n_stage = list1 > list0 ? (tile1 - tile0 + kStageTiles - 1) / kStageTiles : 0;
   uint8_t* ring = smem + warp * kStages * C::kStageBytes;
   uint64_t* bar = bars + warp * kStages;
-  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st
+  const uint32_t nibbles = a.nibbles, c128 = a.c128;
+  int2* desc = descs + warp * kStages;
+  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st, and the positions of its tiles (-1: none)
     uint32_t bytes = 0;
     const uint8_t* src[kStageTiles];
+    int first[kStageTiles];
 #pragma unroll
     for (int k = 0; k < kStageTiles; ++k) {
       const int tile = tile0 + st * kStageTiles + k;
       src[k] = nullptr;
+      first[k] = -1;
       if (tile < tile1) {
         const int2 e = ent[((tile << 4) >> pl) - e0];
         const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
         if (e.x >= 0 && p < u.ctx) {
           src[k] = a.cache + tile_offset(a.pg, e.x, u.h, p, F::kTile);
           bytes += F::kTile;
+          first[k] = p;
         }
       }
     }
+    desc[slot] = make_int2(first[0], first[1]);
     tc::mbar_arrive_expect_tx(bar + slot, bytes);
     const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
     if (src[0] && src[1] == src[0] + F::kTile) {
@@ -333,41 +351,20 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     for (int i = 0; i < kStages; ++i)
       if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, i);
 
-  int slot = 0;
-  uint32_t phase = 0;
-  for (int st = warp; st < n_stage; st += kAttWarps) {
-    if (!tc::mbar_wait(bar + slot, phase, &abort_flag)) {
-      // give the copies in flight the same time each, then leave
-      for (int i = 0, s2 = slot; i < kStages; ++i) {
-        if (st + i * kAttWarps < n_stage) {
-          const unsigned long long t0 = tc::globaltimer();
-          while (!tc::mbar_try_wait(bar + s2, (s2 < slot) ? phase ^ 1 : phase) && tc::globaltimer() - t0 < tc::kWaitNs) {
-          }
-        }
-        s2 = s2 + 1 == kStages ? 0 : s2 + 1;
-      }
-      break;
-    }
-    const uint8_t* buf = ring + slot * C::kStageBytes;
-    // ---- logits of 2 x 16 keys: s[..][nt][0,1]: key g, columns 2 t4, +1;  [2,3]: key g + 8
+  // One stage: 2 x 16 keys.  MASKED: a tile may be missing, and every key is tested against the columns.
+  auto consume = [&](const uint8_t* buf, const int (&first)[kStageTiles], auto masked_c) {
+    constexpr bool MASKED = decltype(masked_c)::value;
+    // ---- logits: s[..][nt][0,1]: key g, columns 2 t4, +1;  [2,3]: key g + 8
     float s[kStageTiles][NT][4];
-    int first[kStageTiles];  // position of the tile's first token, or a value past every limit
-    bool any_tile = false;
 #pragma unroll
     for (int k = 0; k < kStageTiles; ++k) {
-      const int tile = tile0 + st * kStageTiles + k;
-      first[k] = -1;
-      if (tile < tile1) {
-        const int2 e = ent[((tile << 4) >> pl) - e0];
-        const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
-        if (e.x >= 0 && p < u.ctx) first[k] = p;
+      if (MASKED) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[k][nt][c] = -INFINITY;
+        if (first[k] < 0) continue;
       }
-      any_tile |= first[k] >= 0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s[k][nt][c] = -INFINITY;
-      if (first[k] < 0) continue;
       const uint8_t* tb = buf + k * F::kTile;
       float acc[NT][4];
 #pragma unroll
@@ -389,8 +386,8 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         for (int kk = 0; kk < GROUP / 16; ++kk) {
           const int ks = n * (GROUP / 16) + kk;
           const int w = ks >> 1, i = (ks & 1) * 2;
-          const uint32_t a0 = codes2<SUB>(wa[w], i), a1 = codes2<SUB>(wb[w], i);
-          const uint32_t a2 = codes2<SUB>(wa[w], i + 1), a3 = codes2<SUB>(wb[w], i + 1);
+          const uint32_t a0 = codes2<SUB>(wa[w], i, nibbles, c128), a1 = codes2<SUB>(wb[w], i, nibbles, c128);
+          const uint32_t a2 = codes2<SUB>(wa[w], i + 1, nibbles, c128), a3 = codes2<SUB>(wb[w], i + 1, nibbles, c128);
 #pragma unroll
           for (int p = P - 1; p >= 0; --p)
 #pragma unroll
@@ -416,161 +413,180 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         fa *= inv[g];
         fb *= inv[g + 8];
       }
-      const bool masked = first[k] + kTileTokens > fast;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float x = acc[nt][c] * (c < 2 ? fa : fb);
-          if (masked) {
+          if (MASKED) {
             const int key = first[k] + g + (c < 2 ? 0 : 8);
             if (key > last[nt][c & 1] || (key == pos[nt][c & 1] && self[nt][c & 1])) x = -INFINITY;
           }
           s[k][nt][c] = x;
         }
     }
-    if (any_tile) {
-      // ---- the running maximum, moved only when a logit is 2^8 above it
-      float top[NT][2];
-      bool raise = false;
+    // ---- the running maximum, moved only when a logit is 2^8 above it
+    float top[NT][2];
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+#pragma unroll
+        for (int k = 1; k < kStageTiles; ++k) x = fmaxf(fmaxf(x, s[k][nt][c]), s[k][nt][c + 2]);
+        top[nt][c] = x;
+        raise |= x > bar_m[nt][c];
+      }
+    if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float x = s[0][nt][c];
-          x = fmaxf(x, s[0][nt][c + 2]);
+          float x = top[nt][c];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[nt][c], x);
+          const float al = m[nt][c] == mn ? 1.f : exp2f(m[nt][c] - mn);
+          m[nt][c] = mn;
+          base[nt][c] = mn == -INFINITY ? 0.f : mn;
+          bar_m[nt][c] = mn == -INFINITY ? mn : mn + kLazyMax;
+          l[nt][c] *= al;
 #pragma unroll
-          for (int k = 1; k < kStageTiles; ++k) x = fmaxf(fmaxf(x, s[k][nt][c]), s[k][nt][c + 2]);
-          top[nt][c] = x;
-          raise |= x > m[nt][c] + (m[nt][c] == -INFINITY ? 0.f : kLazyMax);
-        }
-      if (__any_sync(0xffffffffu, raise)) {
+          for (int i = 0; i < KS; ++i) {
+            o[nt][i][c] *= al;
+            o[nt][i][c + 2] *= al;
+          }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = top[nt][c];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[nt][c], x);
-            const float al = m[nt][c] == mn ? 1.f : exp2f(m[nt][c] - mn);
-            m[nt][c] = mn;
-            l[nt][c] *= al;
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-              o[nt][i][c] *= al;
-              o[nt][i][c + 2] *= al;
-            }
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-              zs[nt][n][c] *= al;
-              if (!SUB) {
-                cb[SUB ? 0 : nt][SUB ? 0 : n][c] *= al;
-                cb[SUB ? 0 : nt][SUB ? 0 : n][c + 2] *= al;
-              }
+          for (int n = 0; n < NG; ++n) {
+            zs[nt][n][c] *= al;
+            if (!SUB) {
+              cb[SUB ? 0 : nt][SUB ? 0 : n][c] *= al;
+              cb[SUB ? 0 : nt][SUB ? 0 : n][c + 2] *= al;
             }
           }
-      }
-      float fresh[P > 1 ? NT : 1][P > 1 ? KS : 1][4];  // fp32: this stage's sums
-      if (P > 1) {
+        }
+    }
+    float fresh[P > 1 ? NT : 1][P > 1 ? KS : 1][4];  // fp32: this stage's sums
+    if (P > 1) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < KS; ++i)
+        for (int i = 0; i < KS; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c] = 0.f;
-      }
+          for (int c = 0; c < 4; ++c) fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c] = 0.f;
+    }
 #pragma unroll
-      for (int k = 0; k < kStageTiles; ++k) {
-        if (first[k] < 0) continue;
-        const uint8_t* tb = buf + k * F::kTile;
-        const bool masked = first[k] + kTileTokens > fast;
-        float p[NT][4];
+    for (int k = 0; k < kStageTiles; ++k) {
+      if (MASKED && first[k] < 0) continue;
+      const uint8_t* tb = buf + k * F::kTile;
+      float p[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float x = s[k][nt][c] - base[nt][c & 1];
+          p[nt][c] = P > 1 ? exp2f(x) : tc::ex2_approx(x);
+          l[nt][c & 1] += p[nt][c];
+        }
+      const uint32_t* vp = reinterpret_cast<const uint32_t*>(tb + F::kOffVp);
+      uint32_t pf[P][NG][NT][2];  // B fragments of (p s): [0] keys 0..7, [1] keys 8..15
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const uint32_t pa = vp[n * 16 + g], pb = vp[n * 16 + g + 8];
+        const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
+        const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float base = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
-            p[nt][c] = P > 1 ? exp2f(s[k][nt][c] - base) : tc::ex2_approx(s[k][nt][c] - base);
-            l[nt][c & 1] += p[nt][c];
+            const bool out = MASKED && s[k][nt][c] == -INFINITY;  // whatever lies in a masked place
+            w[c] = out ? 0.f : p[nt][c] * (c < 2 ? sa : sb);
+            if (!out) zs[nt][n][c & 1] = fmaf(p[nt][c], c < 2 ? za : zb, zs[nt][n][c & 1]);
           }
-        const uint32_t* vp = reinterpret_cast<const uint32_t*>(tb + F::kOffVp);
-        uint32_t pf[P][NG][NT][2];  // B fragments of (p s): [0] keys 0..7, [1] keys 8..15
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          const uint32_t pa = vp[n * 16 + g], pb = vp[n * 16 + g + 8];
-          const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
-          const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w[4], z[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              w[c] = p[nt][c] * (c < 2 ? sa : sb);
-              z[c] = p[nt][c] * (c < 2 ? za : zb);
-              if (masked && s[k][nt][c] == -INFINITY) w[c] = z[c] = 0.f;  // whatever lies in a masked place
-            }
-            zs[nt][n][0] += z[0] + z[2];
-            zs[nt][n][1] += z[1] + z[3];
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-              const uint32_t lo = tc::pack_bf16x2(w[0], w[1]), hi = tc::pack_bf16x2(w[2], w[3]);
-              pf[i][n][nt][0] = movmatrix(lo);
-              pf[i][n][nt][1] = movmatrix(hi);
-              if (i + 1 < P) {
-                w[0] -= bf16_bits(lo); w[1] -= __uint_as_float(lo & 0xffff0000u);
-                w[2] -= bf16_bits(hi); w[3] -= __uint_as_float(hi & 0xffff0000u);
-              }
+          for (int i = 0; i < P; ++i) {
+            const uint32_t lo = tc::pack_bf16x2(w[0], w[1]), hi = tc::pack_bf16x2(w[2], w[3]);
+            pf[i][n][nt][0] = movmatrix(lo);
+            pf[i][n][nt][1] = movmatrix(hi);
+            if (i + 1 < P) {
+              w[0] -= bf16_bits(lo); w[1] -= __uint_as_float(lo & 0xffff0000u);
+              w[2] -= bf16_bits(hi); w[3] -= __uint_as_float(hi & 0xffff0000u);
             }
           }
-        }
-        const uint8_t* vrow = tb + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8);
-        uint32_t w0[D / 32], w1[D / 32];  // token pairs t4 and t4 + 4
-        lds_words<D / 32>(vrow, w0);
-        lds_words<D / 32>(vrow + 4 * D, w1);
-#pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          // the two tokens of a pair side by side: 16 dims in two words
-          uint32_t r0[2], r1[2];
-          r0[0] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x5410);
-          r0[1] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x7632);
-          r1[0] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x5410);
-          r1[1] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x7632);
-#pragma unroll
-          for (int mm = 0; mm < 4; ++mm) {
-            const int mt = 4 * q + mm, n = mt * 16 / GROUP, i = (mm & 1) * 2;
-            const uint32_t a0 = codes2<SUB>(r0[mm >> 1], i), a1 = codes2<SUB>(r0[mm >> 1], i + 1);
-            const uint32_t a2 = codes2<SUB>(r1[mm >> 1], i), a3 = codes2<SUB>(r1[mm >> 1], i + 1);
-#pragma unroll
-            for (int pc = P - 1; pc >= 0; --pc)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                if (P > 1)
-                  mma16816(fresh[P > 1 ? nt : 0][P > 1 ? mt : 0], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
-                else
-                  mma16816(o[nt][mt], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
-              }
-          }
-        }
-        if (!SUB) {
-          const uint32_t c = 0xc300c300u;  // -128 twice
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816(cb[SUB ? 0 : nt][SUB ? 0 : n], c, c, c, c, pf[0][n][nt][0], pf[0][n][nt][1]);
         }
       }
-      if (P > 1) {
+      const uint8_t* vrow = tb + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8);
+      uint32_t w0[D / 32], w1[D / 32];  // token pairs t4 and t4 + 4
+      lds_words<D / 32>(vrow, w0);
+      lds_words<D / 32>(vrow + 4 * D, w1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int q = 0; q < D / 64; ++q) {
+        // the two tokens of a pair side by side: 16 dims in two words
+        uint32_t r0[2], r1[2];
+        r0[0] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x5410);
+        r0[1] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x7632);
+        r1[0] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x5410);
+        r1[1] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x7632);
 #pragma unroll
-          for (int i = 0; i < KS; ++i)
+        for (int mm = 0; mm < 4; ++mm) {
+          const int mt = 4 * q + mm, n = mt * 16 / GROUP, i = (mm & 1) * 2;
+          const uint32_t a0 = codes2<SUB>(r0[mm >> 1], i, nibbles, c128), a1 = codes2<SUB>(r0[mm >> 1], i + 1, nibbles, c128);
+          const uint32_t a2 = codes2<SUB>(r1[mm >> 1], i, nibbles, c128), a3 = codes2<SUB>(r1[mm >> 1], i + 1, nibbles, c128);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[nt][i][c] += fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c];
+          for (int pc = P - 1; pc >= 0; --pc)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (P > 1)
+                mma16816(fresh[P > 1 ? nt : 0][P > 1 ? mt : 0], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
+              else
+                mma16816(o[nt][mt], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
+            }
+        }
+      }
+      if (!SUB) {
+        const uint32_t c = 0xc300c300u;  // -128 twice
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(cb[SUB ? 0 : nt][SUB ? 0 : n], c, c, c, c, pf[0][n][nt][0], pf[0][n][nt][1]);
       }
     }
+    if (P > 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[nt][i][c] += fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c];
+    }
+  };
+
+  int slot = 0;
+  uint32_t phase = 0;
+  for (int st = warp; st < n_stage; st += kAttWarps) {
+    if (!tc::mbar_wait(bar + slot, phase, &abort_flag)) {
+      // give the copies in flight the same time each, then leave
+      for (int i = 0, s2 = slot; i < kStages; ++i) {
+        if (st + i * kAttWarps < n_stage) {
+          const unsigned long long t0 = tc::globaltimer();
+          while (!tc::mbar_try_wait(bar + s2, (s2 < slot) ? phase ^ 1 : phase) && tc::globaltimer() - t0 < tc::kWaitNs) {
+          }
+        }
+        s2 = s2 + 1 == kStages ? 0 : s2 + 1;
+      }
+      break;
+    }
+    const int2 dsc = desc[slot];
+    const int first[kStageTiles] = {dsc.x, dsc.y};
+    const uint8_t* buf = ring + slot * C::kStageBytes;
+    if (min(dsc.x, dsc.y) >= 0 && max(dsc.x, dsc.y) + kTileTokens <= fast)
+      consume(buf, first, std::false_type());
+    else if (max(dsc.x, dsc.y) >= 0)
+      consume(buf, first, std::true_type());
     __syncwarp();
     if (lane == 0 && st + kStages * kAttWarps < n_stage) issue(st + kStages * kAttWarps, slot);
     if (++slot == kStages) {
