@@ -54,10 +54,10 @@ lsh_status cache_form_dispatch(int D, int group, Fn f) {
   return LSH_ERR_UNSUPPORTED;
 }
 
-// How an attention call is cut: query columns per cached head in tiles of 8 * nt, keys in splits.
+// How an attention call is cut: query columns per cached head in tiles of cw * nt, keys in splits.
 struct AttendPlan {
   long long units;
-  int cols, nt, n_ct, split_tokens, n_splits;
+  int cols, cw, nt, n_ct, split_tokens, n_splits;
 };
 
 inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int max_pages, int page, int n_select) {
@@ -65,8 +65,12 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
   const bool sel = n_select > 0;
   p.units = (long long)B * H * (sel ? T : 1);
   p.cols = sel ? G : G * T;
+  // few columns: several tiles share a fragment (at D 256 two at most: a stage of four would leave an
+  // SM half as many warps)
+  const int least = D == 256 ? 4 : 2;
+  p.cw = p.cols <= 2 ? least : (p.cols <= 4 && (dtype == LSH_BF16 || D == 256)) ? 4 : 8;
   p.nt = (dtype == LSH_BF16 && D <= 128 && p.cols > 8) ? 2 : 1;
-  p.n_ct = (p.cols + 8 * p.nt - 1) / (8 * p.nt);
+  p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
   const long long keys = (long long)(sel ? n_select : max_pages) * page;
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
   long long split = keys * p.units * p.n_ct / ((long long)sms * 12);
@@ -83,11 +87,11 @@ inline size_t attend_plan_bytes(const AttendPlan& p, int D) {
   return n * D * sizeof(float) + (n * 2 * sizeof(float) + 15) / 16 * 16;
 }
 
-template <typename TQ, typename TO, int D, int GROUP, int NT>
+template <typename TQ, int D, int GROUP, int CW, int NT>
 lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   using namespace lsh::cache;
-  using C = AttendCfg<TQ, D, GROUP, NT>;
-  auto kfn = cache_attend_kernel<TQ, TO, D, GROUP, NT>;
+  using C = AttendCfg<TQ, D, GROUP, CW, NT>;
+  auto kfn = cache_attend_kernel<TQ, D, GROUP, CW, NT>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return LSH_ERR_CUDA;
   const long long grid = p.units * p.n_splits * p.n_ct;
@@ -104,7 +108,7 @@ lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<TO, D>, a) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
 }
 
 }  // namespace
@@ -278,6 +282,7 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   a.causal = (mask & LSH_MASK_CAUSAL) ? 1 : 0;
   a.self_mask = (mask & LSH_MASK_SELF) ? 1 : 0;
   a.unit_keys = unit_keys;
+  a.out_f32 = out_dtype == LSH_F32;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.split_tokens = p.split_tokens;
   a.n_splits = p.n_splits;
@@ -290,16 +295,16 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   return cache_form_dispatch(D, group, [&](auto DC, auto GC) -> lsh_status {
     constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
     using bf = __nv_bfloat16;
+    constexpr int kLeast = DD == 256 ? 4 : 2;
     if (dtype == LSH_F32)
-      return out_dtype == LSH_F32 ? launch_cache_attend<float, float, DD, GG, 1>(a, p, s)
-                                  : launch_cache_attend<float, bf, DD, GG, 1>(a, p, s);
+      return p.cw == 8 ? launch_cache_attend<float, DD, GG, 8, 1>(a, p, s)
+                       : launch_cache_attend<float, DD, GG, kLeast, 1>(a, p, s);
+    if (p.cw == kLeast) return launch_cache_attend<bf, DD, GG, kLeast, 1>(a, p, s);
     if constexpr (DD <= 128) {
-      if (p.nt == 2)
-        return out_dtype == LSH_F32 ? launch_cache_attend<bf, float, DD, GG, 2>(a, p, s)
-                                    : launch_cache_attend<bf, bf, DD, GG, 2>(a, p, s);
+      if (p.cw == 4) return launch_cache_attend<bf, DD, GG, 4, 1>(a, p, s);
+      if (p.nt == 2) return launch_cache_attend<bf, DD, GG, 8, 2>(a, p, s);
     }
-    return out_dtype == LSH_F32 ? launch_cache_attend<bf, float, DD, GG, 1>(a, p, s)
-                                : launch_cache_attend<bf, bf, DD, GG, 1>(a, p, s);
+    return launch_cache_attend<bf, DD, GG, 8, 1>(a, p, s);
   });
 }
 

@@ -5,9 +5,15 @@
 // matrix units:  q . K = sum_grp ( s_grp sum_d q_d c_d + z_grp sum_d q_d ),  and
 // the output  O_d = sum_j (p_j s_j) c_jd + sum_j p_j z_j.  So codes 0..15 (exact in
 // bf16) are the A operand of mma.m16n8k16 and the queries (then the weights
-// p_j s_j) its B operand: S^T = K Q^T and O^T = V^T P^T, 8 query columns wide.  With
-// keys as the 16 rows no more than 8 columns are padded, and a group of query heads
-// or several new tokens share every key that is unpacked.
+// p_j s_j) its B operand: S^T = K Q^T and O^T = V^T P^T, 8 columns wide.  With keys as
+// the 16 rows, a group of query heads or several new tokens share every key that is
+// unpacked.
+//
+// A single token has one or two query columns, and all that follows the products (scales,
+// exponentials, weights) would be done for 8.  So a fragment's 8 columns are CW query columns
+// of each of TP = 8 / CW tiles: tile i's products use a B operand that is zero outside its
+// own CW columns, and add into the same fragment.  Column n = i CW + c is a stream of its
+// own with its own maximum and sum; the streams are joined with the warps at the end.
 //
 // A code becomes a bf16 by masking: 0x4300 | c is 128 + c.  For bf16 queries the 128 is
 // taken out on the other side: S starts at -128 sum q, and one more product per group
@@ -16,9 +22,9 @@
 // there 128 is subtracted from the codes and the sums leave the matrix unit every
 // 32 tokens, so that its accumulation does not show.
 //
-// Every warp is a pipeline of its own: a lane copies 32 tokens (one or two
-// cp.async.bulk, codes and parameters together) into the warp's ring, kStages deep, and
-// the warp consumes them without a block barrier.  A split's warps meet once, at its end.
+// Every warp is a pipeline of its own: a lane copies ST tiles (cp.async.bulk, codes
+// and parameters together, one copy for tiles that lie side by side) into the warp's ring,
+// kStages deep, and the warp consumes them without a block barrier.  A split's warps meet once, at its end.
 // The maximum moves only when a logit exceeds it by 2^8: weights up to 256 cost nothing
 // in float, and the 32-lane maximum and the rescaling of O are left out of most steps.
 #pragma once
@@ -33,8 +39,7 @@ namespace cache {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
-constexpr int kStageTiles = 2;       // 32 tokens a copy
-constexpr int kStages = 3;           // copies in flight per warp
+constexpr int kStages = 2;           // stages in flight per warp
 constexpr int kMaxEntries = 512;     // pages of a split
 constexpr float kLazyMax = 8.f;
 
@@ -46,7 +51,7 @@ struct AttendArgs {
   float* lse;               // [B, H * G, T]
   float *part_o, *part_ml;  // [units, n_splits, cols, D], [units, n_splits, cols, 2]
   int B, G, n_select;
-  int causal, self_mask, unit_keys;
+  int causal, self_mask, unit_keys, out_f32;
   float scale_log2;         // scale * log2(e)
   int split_tokens, n_splits, n_ct, cols;
   uint32_t nibbles, c128;   // 0x000f000f, 0x43004300 (see codes2)
@@ -129,43 +134,49 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-template <typename TQ, int D, int GROUP, int NT>
+// CW: query columns of a tile in a fragment (2, 4 or 8); NT: fragments side by side (CW 8 only).
+template <typename TQ, int D, int GROUP, int CW, int NT>
 struct AttendCfg {
   using F = Fmt<D, GROUP>;
+  static_assert(CW == 8 || NT == 1, "more than 8 columns go in whole fragments");
   static constexpr bool kF32 = sizeof(TQ) == 4;
   static constexpr int kPieces = kF32 ? 3 : 1;
   // 128 taken out of the codes: always in fp32; at D 256 the -128 products' accumulators would not fit
   static constexpr bool kSub = kF32 || D == 256;
-  static constexpr int kKs = D / 16;  // k steps of Q K^T, m tiles of V^T P^T
-  static constexpr int kCols = 8 * NT;
-  static constexpr int kStageBytes = kStageTiles * F::kTile;
+  static constexpr int kKs = D / 16;             // k steps of Q K^T, m tiles of V^T P^T
+  static constexpr int kTp = 8 / CW;             // tiles of a fragment
+  static constexpr int kSt = kTp > 2 ? kTp : 2;  // tiles of a stage
+  static constexpr int kSf = kSt / kTp;          // fragments of a stage
+  static constexpr int kQ = CW * NT;             // query columns of a CTA
+  static constexpr int kCols = 8 * NT;           // streams of a warp
+  static constexpr int kStageBytes = kSt * F::kTile;
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
   static constexpr int kMerge = kAttWarps * kCols * D * 4;
   static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kOffQs = kOffQ + kPieces * NT * kKs * 32 * 8;
-  static constexpr int kOffMl = kOffQs + kCols * F::kGroups * 4;
+  static constexpr int kOffQs = kOffQ + kPieces * NT * kTp * kKs * 32 * 8;
+  static constexpr int kOffMl = kOffQs + kQ * F::kGroups * 4;
   static constexpr int kOffEnt = kOffMl + kAttWarps * kCols * 8;
   static constexpr int kOffBar = kOffEnt + kMaxEntries * 8;
   static constexpr int kOffDesc = kOffBar + kAttWarps * kStages * 8;
-  static constexpr int kSmem = kOffDesc + kAttWarps * kStages * 8;
-  static constexpr int kRegQ = kPieces * NT * kKs * 2 <= 32;
+  static constexpr int kSmem = kOffDesc + kAttWarps * kStages * kSt * 4;
+  static_assert(kOffMl % 8 == 0 && kOffBar % 8 == 0 && kOffDesc % 8 == 0, "alignment");
 };
 
-template <typename TQ, typename TO, int D, int GROUP, int NT>
+template <typename TQ, int D, int GROUP, int CW, int NT>
 __global__ void __launch_bounds__(kAttThreads)
 cache_attend_kernel(const __grid_constant__ AttendArgs a) {
-  using C = AttendCfg<TQ, D, GROUP, NT>;
+  using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   using F = Fmt<D, GROUP>;
-  constexpr int NG = F::kGroups, KS = C::kKs, P = C::kPieces;
+  constexpr int NG = F::kGroups, KS = C::kKs, P = C::kPieces, TP = C::kTp, ST = C::kSt, SF = C::kSf;
   constexpr bool SUB = C::kSub;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int abort_flag;
-  uint2* qf = reinterpret_cast<uint2*>(smem + C::kOffQ);
+  uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQ);
   float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   int2* ent = reinterpret_cast<int2*>(smem + C::kOffEnt);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  int2* descs = reinterpret_cast<int2*>(smem + C::kOffDesc);
+  int* descs = reinterpret_cast<int*>(smem + C::kOffDesc);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int ct = blockIdx.x % a.n_ct;
@@ -173,7 +184,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   const int unit = (int)(us / a.n_splits), split = (int)(us - (long long)unit * a.n_splits);
   const Unit u = unit_of(a, unit);
   const bool sel = a.selected != nullptr;
-  const int col0 = ct * C::kCols;
+  const int col0 = ct * C::kQ;
   const int list0 = split * a.split_tokens;
   const int list1 = min(u.n_list, list0 + a.split_tokens);
   if (list0 >= list1 && split > 0) return;  // the first split always answers, with nothing if there is nothing
@@ -197,9 +208,10 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     return static_cast<const TQ*>(a.q) + (((long long)u.b * a.pg.H + u.h) * a.G + gg) * (long long)a.pg.T * D +
            (long long)tt * D;
   };
+  // B operands: of fragment column n = i CW + c the query column c, for tile i; zero for the others
   for (int i = tid; i < NT * KS * 32; i += kAttThreads) {
     const int l = i & 31, ks = (i >> 5) % KS, nt = (i >> 5) / KS;
-    const int col = col0 + nt * 8 + (l >> 2);
+    const int n = l >> 2, col = col0 + nt * CW + n % CW;
     const int d0 = 32 * (ks >> 1) + 8 * (ks & 1) + 2 * (l & 3);
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     if (col < a.cols) {
@@ -215,13 +227,16 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         y[k] = __bfloat162float(__float2bfloat16_rn(x[k]));
         x[k] -= y[k];
       }
-      qf[((p * NT + nt) * KS + ks) * 32 + l] = make_uint2(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]));
+      const uint2 w = make_uint2(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]));
+#pragma unroll
+      for (int t = 0; t < TP; ++t)
+        reinterpret_cast<uint2*>(qf + (((p * NT + nt) * TP + t) * (KS / 2) + (ks >> 1)) * 32 + l)[ks & 1] =
+            n / CW == t ? w : make_uint2(0, 0);
     }
   }
   // sums of the queries by group: 16 threads a column, D/16 dims each
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int cc = nt * 8 + (tid >> 4), j = tid & 15;
+  for (int cc = tid >> 4; cc < C::kQ; cc += kAttThreads / 16) {
+    const int j = tid & 15;
     float x = 0.f;
     if (col0 + cc < a.cols) {
       const TQ* q = q_row(col0 + cc) + j * (D / 16);
@@ -229,13 +244,14 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       for (int d = 0; d < D / 16; ++d) x += to_f32<TQ>(q[d]);
     }
 #pragma unroll
-    for (int o = 1; o < 16 / NG; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 1; o < 16 / NG; o <<= 1) x += __shfl_xor_sync(0xffffu << (tid & 16), x, o);
     if (j % (16 / NG) == 0) qs[cc * NG + j / (16 / NG)] = x;
   }
   tc::fence_mbar_init();
   __syncthreads();
 
-  // ---- the lane's query columns (C fragment: columns 2 t4 and 2 t4 + 1 of each 8) ------------------
+  // ---- the lane's streams (C fragment: columns 2 t4 and 2 t4 + 1 of each 8) -------------------------
+  const int my_tile = 2 * t4 / CW;  // the tile of a fragment that both belong to
   int pos[NT][2], last[NT][2];  // position; largest admissible position
   bool self[NT][2];             // whether its own key is masked
   int fast = u.ctx;             // tiles that end at or below are admissible to every column
@@ -243,7 +259,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int col = col0 + nt * 8 + 2 * t4 + k;
+      const int col = col0 + nt * CW + (2 * t4 + k) % CW;
       const int tt = sel ? u.t : col / a.G;
       const bool live = col < a.cols && row_live(u, tt);
       pos[nt][k] = live ? u.start + tt : -1;
@@ -271,22 +287,13 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) fast = min(fast, __shfl_xor_sync(0xffffffffu, fast, o));
 
-  uint2 qr[C::kRegQ ? P * NT * KS : 1];
-  if (C::kRegQ) {
-#pragma unroll
-    for (int i = 0; i < P * NT * KS; ++i) qr[i] = qf[i * 32 + lane];
-  }
-  auto qfrag = [&](int p, int nt, int ks) -> uint2 {
-    const int i = (p * NT + nt) * KS + ks;
-    return C::kRegQ ? qr[C::kRegQ ? i : 0] : qf[i * 32 + lane];
-  };
   float qsum[NT][NG][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) qsum[nt][n][k] = qs[(nt * 8 + 2 * t4 + k) * NG + n];
+      for (int k = 0; k < 2; ++k) qsum[nt][n][k] = qs[(nt * CW + (2 * t4 + k) % CW) * NG + n];
 
   float m[NT][2], base[NT][2], bar_m[NT][2], l[NT][2];  // maximum; what is subtracted; where it has to move
   float o[NT][KS][4], zs[NT][NG][2], cb[SUB ? 1 : NT][SUB ? 1 : NG][4];
@@ -312,90 +319,98 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 
   // ---- the warp's pipeline ------------------------------------------------------------------------
   const int tile0 = list0 >> 4, tile1 = (list1 + 15) >> 4;  // tiles in list order
-  const int n_stage = list1 > list0 ? (tile1 - tile0 + kStageTiles - 1) / kStageTiles : 0;
+  const int n_stage = list1 > list0 ? (tile1 - tile0 + ST - 1) / ST : 0;
   uint8_t* ring = smem + warp * kStages * C::kStageBytes;
   uint64_t* bar = bars + warp * kStages;
   const uint32_t nibbles = a.nibbles, c128 = a.c128;
-  int2* desc = descs + warp * kStages;
+  int* desc = descs + warp * kStages * ST;
   auto issue = [&](int st, int slot) {  // lane 0: copies of stage st, and the positions of its tiles (-1: none)
     uint32_t bytes = 0;
-    const uint8_t* src[kStageTiles];
-    int first[kStageTiles];
+    const uint8_t* src[ST];
 #pragma unroll
-    for (int k = 0; k < kStageTiles; ++k) {
-      const int tile = tile0 + st * kStageTiles + k;
+    for (int k = 0; k < ST; ++k) {
+      const int tile = tile0 + st * ST + k;
       src[k] = nullptr;
-      first[k] = -1;
+      int first = -1;
       if (tile < tile1) {
         const int2 e = ent[((tile << 4) >> pl) - e0];
         const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
         if (e.x >= 0 && p < u.ctx) {
           src[k] = a.cache + tile_offset(a.pg, e.x, u.h, p, F::kTile);
           bytes += F::kTile;
-          first[k] = p;
+          first = p;
         }
       }
+      desc[slot * ST + k] = first;
     }
-    desc[slot] = make_int2(first[0], first[1]);
     tc::mbar_arrive_expect_tx(bar + slot, bytes);
     const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
-    if (src[0] && src[1] == src[0] + F::kTile) {
-      bulk_load(dst, src[0], kStageTiles * F::kTile, bar + slot);
-    } else {
+    int from = 0;  // runs of tiles side by side
 #pragma unroll
-      for (int k = 0; k < kStageTiles; ++k)
-        if (src[k]) bulk_load(dst + k * F::kTile, src[k], F::kTile, bar + slot);
+    for (int k = 1; k <= ST; ++k) {
+      if (k < ST && src[k] && src[k] == src[k - 1] + F::kTile) continue;
+      if (src[k - 1]) bulk_load(dst + from * F::kTile, src[k - 1] - (k - 1 - from) * F::kTile, (k - from) * F::kTile, bar + slot);
+      from = k;
     }
   };
   if (lane == 0)
     for (int i = 0; i < kStages; ++i)
       if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, i);
 
-  // One stage: 2 x 16 keys.  MASKED: a tile may be missing, and every key is tested against the columns.
-  auto consume = [&](const uint8_t* buf, const int (&first)[kStageTiles], auto masked_c) {
+  // One stage of ST tiles.  MASKED: a tile may be missing, and every key is tested against the columns.
+  auto consume = [&](const uint8_t* buf, const int* first, auto masked_c) {  // first: positions, in shared memory
     constexpr bool MASKED = decltype(masked_c)::value;
-    // ---- logits: s[..][nt][0,1]: key g, columns 2 t4, +1;  [2,3]: key g + 8
-    float s[kStageTiles][NT][4];
+    // ---- logits: s[f][nt][0,1]: key g of the lane's tile, columns 2 t4, +1;  [2,3]: key g + 8
+    float s[SF][NT][4];
 #pragma unroll
-    for (int k = 0; k < kStageTiles; ++k) {
-      if (MASKED) {
+    for (int f = 0; f < SF; ++f) {
+      float part[NT][NG][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) s[k][nt][c] = -INFINITY;
-        if (first[k] < 0) continue;
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) part[nt][n][c] = SUB ? 0.f : -128.f * qsum[nt][n][c & 1];
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        const int k = f * TP + i;
+        if (MASKED && first[k] < 0) continue;
+        const uint8_t* tb = buf + k * F::kTile;
+        uint32_t wa[D / 32], wb[D / 32];
+        lds_words<D / 32>(tb + g * (D / 2) + t4 * (D / 8), wa);
+        lds_words<D / 32>(tb + (g + 8) * (D / 2) + t4 * (D / 8), wb);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {  // two k steps a word
+          const int n = w * 32 / GROUP;
+          uint32_t x[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[e][0] = codes2<SUB>(wa[w], 2 * e, nibbles, c128);
+            x[e][1] = codes2<SUB>(wb[w], 2 * e, nibbles, c128);
+            x[e][2] = codes2<SUB>(wa[w], 2 * e + 1, nibbles, c128);
+            x[e][3] = codes2<SUB>(wb[w], 2 * e + 1, nibbles, c128);
+          }
+#pragma unroll
+          for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4 b = qf[(((p * NT + nt) * TP + i) * (KS / 2) + w) * 32 + lane];
+              mma16816(part[nt][n], x[0][0], x[0][1], x[0][2], x[0][3], b.x, b.y);
+              mma16816(part[nt][n], x[1][0], x[1][1], x[1][2], x[1][3], b.z, b.w);
+            }
+        }
       }
-      const uint8_t* tb = buf + k * F::kTile;
+      const int mine = f * TP + my_tile;
+      const int first_mine = MASKED ? first[mine] : 0;
+      const uint8_t* tb = buf + mine * F::kTile;
+      const uint32_t* kp = reinterpret_cast<const uint32_t*>(tb + F::kOffKp);
       float acc[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
-      uint32_t wa[D / 32], wb[D / 32];
-      lds_words<D / 32>(tb + g * (D / 2) + t4 * (D / 8), wa);
-      lds_words<D / 32>(tb + (g + 8) * (D / 2) + t4 * (D / 8), wb);
-      const uint32_t* kp = reinterpret_cast<const uint32_t*>(tb + F::kOffKp);
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        float part[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) part[nt][c] = SUB ? 0.f : -128.f * qsum[nt][n][c & 1];
-#pragma unroll
-        for (int kk = 0; kk < GROUP / 16; ++kk) {
-          const int ks = n * (GROUP / 16) + kk;
-          const int w = ks >> 1, i = (ks & 1) * 2;
-          const uint32_t a0 = codes2<SUB>(wa[w], i, nibbles, c128), a1 = codes2<SUB>(wb[w], i, nibbles, c128);
-          const uint32_t a2 = codes2<SUB>(wa[w], i + 1, nibbles, c128), a3 = codes2<SUB>(wb[w], i + 1, nibbles, c128);
-#pragma unroll
-          for (int p = P - 1; p >= 0; --p)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 b = qfrag(p, nt, ks);
-              mma16816(part[nt], a0, a1, a2, a3, b.x, b.y);
-            }
-        }
         const uint32_t pa = kp[n * 16 + g], pb = kp[n * 16 + g + 8];
         const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
         const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
@@ -403,8 +418,8 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            acc[nt][c] = fmaf(sa, part[nt][c], fmaf(za, qsum[nt][n][c], acc[nt][c]));
-            acc[nt][2 + c] = fmaf(sb, part[nt][2 + c], fmaf(zb, qsum[nt][n][c], acc[nt][2 + c]));
+            acc[nt][c] = fmaf(sa, part[nt][n][c], fmaf(za, qsum[nt][n][c], acc[nt][c]));
+            acc[nt][2 + c] = fmaf(sb, part[nt][n][2 + c], fmaf(zb, qsum[nt][n][c], acc[nt][2 + c]));
           }
       }
       float fa = a.scale_log2, fb = a.scale_log2;
@@ -419,10 +434,10 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         for (int c = 0; c < 4; ++c) {
           float x = acc[nt][c] * (c < 2 ? fa : fb);
           if (MASKED) {
-            const int key = first[k] + g + (c < 2 ? 0 : 8);
-            if (key > last[nt][c & 1] || (key == pos[nt][c & 1] && self[nt][c & 1])) x = -INFINITY;
+            const int key = first_mine + g + (c < 2 ? 0 : 8);
+            if (first_mine < 0 || key > last[nt][c & 1] || (key == pos[nt][c & 1] && self[nt][c & 1])) x = -INFINITY;
           }
-          s[k][nt][c] = x;
+          s[f][nt][c] = x;
         }
     }
     // ---- the running maximum, moved only when a logit is 2^8 above it
@@ -434,7 +449,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       for (int c = 0; c < 2; ++c) {
         float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
 #pragma unroll
-        for (int k = 1; k < kStageTiles; ++k) x = fmaxf(fmaxf(x, s[k][nt][c]), s[k][nt][c + 2]);
+        for (int f = 1; f < SF; ++f) x = fmaxf(fmaxf(x, s[f][nt][c]), s[f][nt][c + 2]);
         top[nt][c] = x;
         raise |= x > bar_m[nt][c];
       }
@@ -478,20 +493,18 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           for (int c = 0; c < 4; ++c) fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c] = 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < kStageTiles; ++k) {
-      if (MASKED && first[k] < 0) continue;
-      const uint8_t* tb = buf + k * F::kTile;
+    for (int f = 0; f < SF; ++f) {
       float p[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float x = s[k][nt][c] - base[nt][c & 1];
+          const float x = s[f][nt][c] - base[nt][c & 1];
           p[nt][c] = P > 1 ? exp2f(x) : tc::ex2_approx(x);
           l[nt][c & 1] += p[nt][c];
         }
-      const uint32_t* vp = reinterpret_cast<const uint32_t*>(tb + F::kOffVp);
-      uint32_t pf[P][NG][NT][2];  // B fragments of (p s): [0] keys 0..7, [1] keys 8..15
+      const uint32_t* vp = reinterpret_cast<const uint32_t*>(buf + (f * TP + my_tile) * F::kTile + F::kOffVp);
+      uint32_t pf[P][NG][NT][2];  // B fragments of (p s): [0] keys 0..7, [1] keys 8..15 of every column's tile
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const uint32_t pa = vp[n * 16 + g], pb = vp[n * 16 + g + 8];
@@ -502,7 +515,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           float w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const bool out = MASKED && s[k][nt][c] == -INFINITY;  // whatever lies in a masked place
+            const bool out = MASKED && s[f][nt][c] == -INFINITY;  // whatever lies in a masked place
             w[c] = out ? 0.f : p[nt][c] * (c < 2 ? sa : sb);
             if (!out) zs[nt][n][c & 1] = fmaf(p[nt][c], c < 2 ? za : zb, zs[nt][n][c & 1]);
           }
@@ -518,34 +531,6 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           }
         }
       }
-      const uint8_t* vrow = tb + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8);
-      uint32_t w0[D / 32], w1[D / 32];  // token pairs t4 and t4 + 4
-      lds_words<D / 32>(vrow, w0);
-      lds_words<D / 32>(vrow + 4 * D, w1);
-#pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        // the two tokens of a pair side by side: 16 dims in two words
-        uint32_t r0[2], r1[2];
-        r0[0] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x5410);
-        r0[1] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x7632);
-        r1[0] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x5410);
-        r1[1] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x7632);
-#pragma unroll
-        for (int mm = 0; mm < 4; ++mm) {
-          const int mt = 4 * q + mm, n = mt * 16 / GROUP, i = (mm & 1) * 2;
-          const uint32_t a0 = codes2<SUB>(r0[mm >> 1], i, nibbles, c128), a1 = codes2<SUB>(r0[mm >> 1], i + 1, nibbles, c128);
-          const uint32_t a2 = codes2<SUB>(r1[mm >> 1], i, nibbles, c128), a3 = codes2<SUB>(r1[mm >> 1], i + 1, nibbles, c128);
-#pragma unroll
-          for (int pc = P - 1; pc >= 0; --pc)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (P > 1)
-                mma16816(fresh[P > 1 ? nt : 0][P > 1 ? mt : 0], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
-              else
-                mma16816(o[nt][mt], a0, a1, a2, a3, pf[pc][n][nt][0], pf[pc][n][nt][1]);
-            }
-        }
-      }
       if (!SUB) {
         const uint32_t c = 0xc300c300u;  // -128 twice
 #pragma unroll
@@ -553,6 +538,49 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma16816(cb[SUB ? 0 : nt][SUB ? 0 : n], c, c, c, c, pf[0][n][nt][0], pf[0][n][nt][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < TP; ++i) {
+        const int k = f * TP + i;
+        if (MASKED && first[k] < 0) continue;
+        const uint8_t* tb = buf + k * F::kTile;
+        uint32_t pb[P][NG][NT][2];  // the tile's own columns
+#pragma unroll
+        for (int pc = 0; pc < P; ++pc)
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) pb[pc][n][nt][e] = TP == 1 || g / CW == i ? pf[pc][n][nt][e] : 0u;
+        const uint8_t* vrow = tb + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8);
+        uint32_t w0[D / 32], w1[D / 32];  // token pairs t4 and t4 + 4
+        lds_words<D / 32>(vrow, w0);
+        lds_words<D / 32>(vrow + 4 * D, w1);
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+          // the two tokens of a pair side by side: 16 dims in two words
+          uint32_t r0[2], r1[2];
+          r0[0] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x5410);
+          r0[1] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x7632);
+          r1[0] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x5410);
+          r1[1] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x7632);
+#pragma unroll
+          for (int mm = 0; mm < 4; ++mm) {
+            const int mt = 4 * q + mm, n = mt * 16 / GROUP, x = (mm & 1) * 2;
+            const uint32_t a0 = codes2<SUB>(r0[mm >> 1], x, nibbles, c128);
+            const uint32_t a1 = codes2<SUB>(r0[mm >> 1], x + 1, nibbles, c128);
+            const uint32_t a2 = codes2<SUB>(r1[mm >> 1], x, nibbles, c128);
+            const uint32_t a3 = codes2<SUB>(r1[mm >> 1], x + 1, nibbles, c128);
+#pragma unroll
+            for (int pc = P - 1; pc >= 0; --pc)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float(&dst)[4] = P > 1 ? fresh[P > 1 ? nt : 0][P > 1 ? mt : 0] : o[nt][mt];
+                mma16816(dst, a0, a1, a2, a3, pb[pc][n][nt][0], pb[pc][n][nt][1]);
+              }
+          }
+        }
       }
     }
     if (P > 1) {
@@ -580,12 +608,17 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       }
       break;
     }
-    const int2 dsc = desc[slot];
-    const int first[kStageTiles] = {dsc.x, dsc.y};
+    const int* first = desc + slot * ST;
+    int lo = first[0], hi = lo;
+#pragma unroll
+    for (int k = 1; k < ST; ++k) {
+      lo = min(lo, first[k]);
+      hi = max(hi, first[k]);
+    }
     const uint8_t* buf = ring + slot * C::kStageBytes;
-    if (min(dsc.x, dsc.y) >= 0 && max(dsc.x, dsc.y) + kTileTokens <= fast)
+    if (lo >= 0 && hi + kTileTokens <= fast)
       consume(buf, first, std::false_type());
-    else if (max(dsc.x, dsc.y) >= 0)
+    else if (hi >= 0)
       consume(buf, first, std::true_type());
     __syncwarp();
     if (lane == 0 && st + kStages * kAttWarps < n_stage) issue(st + kStages * kAttWarps, slot);
@@ -624,25 +657,31 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       }
     }
   __syncthreads();
-  for (int i = tid; i < C::kCols * D; i += kAttThreads) {
+  for (int i = tid; i < C::kQ * D; i += kAttThreads) {
     const int cc = i / D, d = i - cc * D, col = col0 + cc;
     if (col >= a.cols) break;
+    const int n0 = NT > 1 ? cc : cc % CW;  // its first stream; the others CW further each
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) mx = fmaxf(mx, ml[w * C::kCols + cc].x);
+    for (int w = 0; w < kAttWarps * TP; ++w) mx = fmaxf(mx, ml[w / TP * C::kCols + n0 + w % TP * CW].x);
     float sum = 0.f, x = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-      const float2 v = ml[w * C::kCols + cc];
+    for (int w = 0; w < kAttWarps * TP; ++w) {
+      const int j = w / TP * C::kCols + n0 + w % TP * CW;
+      const float2 v = ml[j];
       const float f = v.x == mx ? 1.f : exp2f(v.x - mx);
       sum = fmaf(v.y, f, sum);
-      x = fmaf(om[(w * C::kCols + cc) * D + d], f, x);
+      x = fmaf(om[j * D + d], f, x);
     }
     if (a.n_splits == 1) {
       const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
       const long long row = (((long long)u.b * a.pg.H + u.h) * a.G + gg) * a.pg.T + tt;
       if (!row_live(u, tt)) sum = 0.f;
-      static_cast<TO*>(a.out)[row * D + d] = from_f32<TO>(sum == 0.f ? 0.f : x / sum);
+      x = sum == 0.f ? 0.f : x / sum;
+      if (a.out_f32)
+        static_cast<float*>(a.out)[row * D + d] = x;
+      else
+        static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(x);
       if (d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
     } else {
       const long long pi = ((long long)unit * a.n_splits + split) * a.cols + col;
@@ -655,7 +694,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 // Joins the splits of a column: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
 constexpr int kJoinThreads = 128;
 
-template <typename TO, int D>
+template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;  // 4 dims a thread, the splits dealt out
   __shared__ float4 so[kParts][kLanes];
@@ -703,9 +742,13 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
   const long long row = (((long long)u.b * a.pg.H + u.h) * a.G + gg) * a.pg.T + tt;
   if (!row_live(u, tt)) sum = 0.f;
-  TO* out = static_cast<TO*>(a.out) + row * D + 4 * j;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = from_f32<TO>(sum == 0.f ? 0.f : r[i] / sum);
+  for (int i = 0; i < 4; ++i) r[i] = sum == 0.f ? 0.f : r[i] / sum;
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 4 * j) = make_float4(r[0], r[1], r[2], r[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * j) =
+        make_uint2(tc::pack_bf16x2(r[0], r[1]), tc::pack_bf16x2(r[2], r[3]));
   if (j == 0) a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
