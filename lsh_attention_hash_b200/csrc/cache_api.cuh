@@ -54,11 +54,14 @@ lsh_status cache_form_dispatch(int D, int group, Fn f) {
   return LSH_ERR_UNSUPPORTED;
 }
 
-// How an attention call is cut: query columns per cached head in tiles of cw * nt, keys in splits.
+// How an attention call is cut: query columns per cached head in tiles of cw * nt, the work over
+// at most max_ctas CTAs (what the kernel's registers and shared memory allow may be fewer).
 struct AttendPlan {
-  long long units;
-  int cols, cw, nt, n_ct, split_tokens, n_splits;
+  long long units, blocks;  // (cached head [, row]) of all sequences; blocks of all items with full tables
+  int cols, cw, nt, n_ct, max_ctas;
 };
+
+constexpr int kMaxCtasPerSm = 6;
 
 inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int max_pages, int page, int n_select) {
   AttendPlan p;
@@ -72,19 +75,17 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
   p.nt = (dtype == LSH_BF16 && D <= 128 && p.cols > 8) ? 2 : 1;
   p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
   const long long keys = (long long)(sel ? n_select : max_pages) * page;
+  const int block = lsh::cache::kBlockTiles * lsh::cache::kTileTokens;
+  p.blocks = p.units * p.n_ct * ((keys + block - 1) / block);
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
-  long long split = keys * p.units * p.n_ct / ((long long)sms * 12);
-  split = (split + 255) / 256 * 256;
-  split = std::min<long long>(std::max<long long>(split, 256), 4096);
-  p.split_tokens = (int)split;
-  p.n_splits = (int)std::max<long long>(1, (keys + split - 1) / split);
+  p.max_ctas = (int)std::max<long long>(1, std::min<long long>(p.blocks, (long long)sms * kMaxCtasPerSm));
   return p;
 }
 
+// Two pieces per CTA: unnormalised outputs, then (maximum, sum).
 inline size_t attend_plan_bytes(const AttendPlan& p, int D) {
-  if (p.n_splits <= 1) return 0;
-  const size_t n = (size_t)p.units * p.n_splits * p.cols;
-  return n * D * sizeof(float) + (n * 2 * sizeof(float) + 15) / 16 * 16;
+  const size_t n = (size_t)p.max_ctas * 2 * p.cw * p.nt;
+  return n * D * sizeof(float) + n * 2 * sizeof(float);
 }
 
 template <typename TQ, int D, int GROUP, int CW, int NT>
@@ -94,11 +95,12 @@ lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, c
   auto kfn = cache_attend_kernel<TQ, D, GROUP, CW, NT>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return LSH_ERR_CUDA;
-  const long long grid = p.units * p.n_splits * p.n_ct;
-  kfn<<<(unsigned)grid, kAttThreads, C::kSmem, s>>>(a);
+  static_assert(C::kCtas >= 1 && C::kCtas <= kMaxCtasPerSm, "workspace is sized for it");
+  const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
+  a.nc = std::min(p.max_ctas, sms * C::kCtas);
+  kfn<<<a.nc, kAttThreads, C::kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
-  if (p.n_splits == 1) return LSH_OK;
-  // the join may be set up while the last splits run; it waits for them before it reads
+  // the join may be set up while the last CTAs run; it waits for them before it reads
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.units * p.cols));
   cfg.blockDim = dim3(kJoinThreads);
@@ -263,10 +265,10 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
     return LSH_ERR_ALIGN;
   if ((long long)B * Hq * T == 0) return LSH_OK;
   const AttendPlan p = attend_plan(dtype, B, H, Hq / H, T, D, max_pages, page, n_select);
-  if (p.units * p.n_splits * p.n_ct >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if (p.units * p.cols >= (1ll << 31) || p.units * p.n_ct >= (1ll << 31)) return LSH_ERR_SHAPE;
   const size_t need = attend_plan_bytes(p, D);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return LSH_ERR_WORKSPACE;
-  if (need > 0 && !aligned16(workspace)) return LSH_ERR_ALIGN;
+  if (!workspace || workspace_bytes < need) return LSH_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LSH_ERR_ALIGN;
   if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)D);
   lsh::cache::AttendArgs a;
   a.q = q;
@@ -275,7 +277,7 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   a.out = out;
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = need ? a.part_o + (size_t)p.units * p.n_splits * p.cols * D : nullptr;
+  a.part_ml = a.part_o + (size_t)p.max_ctas * 2 * p.cw * p.nt * D;
   a.B = B;
   a.G = Hq / H;
   a.n_select = n_select;
@@ -284,10 +286,9 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   a.unit_keys = unit_keys;
   a.out_f32 = out_dtype == LSH_F32;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.split_tokens = p.split_tokens;
-  a.n_splits = p.n_splits;
   a.n_ct = p.n_ct;
   a.cols = p.cols;
+  a.tile_cols = p.cw * p.nt;
   a.nibbles = 0x000f000fu;
   a.c128 = 0x43004300u;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);

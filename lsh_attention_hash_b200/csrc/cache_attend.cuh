@@ -1,5 +1,6 @@
 // Attention of new tokens over the 4-bit cache: one pass with the running maximum
-// and sum of the softmax, split over the keys and joined by a second small kernel.
+// and sum of the softmax, the keys of all sequences dealt out evenly over the SMs and the
+// pieces joined by a second small kernel.
 //
 // With K = z + s c by groups of dims, a query's logit needs only whole codes on the
 // matrix units:  q . K = sum_grp ( s_grp sum_d q_d c_d + z_grp sum_d q_d ),  and
@@ -24,9 +25,15 @@
 //
 // Every warp is a pipeline of its own: a lane copies ST tiles (cp.async.bulk, codes
 // and parameters together, one copy for tiles that lie side by side) into the warp's ring,
-// kStages deep, and the warp consumes them without a block barrier.  A split's warps meet once, at its end.
+// and the warp consumes them without a block barrier.  A piece's warps meet once, at its end.
 // The maximum moves only when a logit exceeds it by 2^8: weights up to 256 cost nothing
 // in float, and the 32-lane maximum and the rescaling of O are left out of most steps.
+//
+// The work is the list of all (cached head, column tile) items, with the row too when pages are
+// selected, each of ceil(keys / 128) blocks; CTA c of NC takes blocks [c W / NC, (c + 1) W / NC) of
+// it, whatever the lengths are, so one wave of CTAs ends together.  An item inside one CTA is
+// written out there; the pieces of any other go to the workspace (a CTA has two at most: its
+// first and its last) and the join adds them up in order.
 #pragma once
 
 #include <type_traits>
@@ -39,8 +46,8 @@ namespace cache {
 
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
-constexpr int kStages = 2;           // stages in flight per warp
-constexpr int kMaxEntries = 512;     // pages of a split
+constexpr int kMaxEntries = 256;     // pages looked up at a time
+constexpr int kBlockTiles = 8;       // 128 tokens: what the work is dealt out in
 constexpr float kLazyMax = 8.f;
 
 struct AttendArgs {
@@ -49,40 +56,88 @@ struct AttendArgs {
   const int32_t* selected;  // [B, H, T, n_select] or null
   void* out;                // [B, H * G, T, D]
   float* lse;               // [B, H * G, T]
-  float *part_o, *part_ml;  // [units, n_splits, cols, D], [units, n_splits, cols, 2]
+  float *part_o, *part_ml;  // [NC, 2, cols of a tile, D], [NC, 2, cols of a tile, 2]
   int B, G, n_select;
   int causal, self_mask, unit_keys, out_f32;
   float scale_log2;         // scale * log2(e)
-  int split_tokens, n_splits, n_ct, cols;
+  int nc, n_ct, cols, tile_cols;  // CTAs; column tiles, all columns, columns of a tile
   uint32_t nibbles, c128;   // 0x000f000f, 0x43004300 (see codes2)
   Pages pg;
 };
 
-// What a unit (a cached head of a sequence; with selection also one new token) attends to.
-struct Unit {
-  int b, h, t;        // t: the row with selection, else 0
-  int ctx, start;     // tokens in the cache, position of row 0
-  int n_new;
-  int n_list;         // tokens in list order: the positions themselves, or those of the selected pages
+// A sequence's part of the work: items of nb blocks each.  Without selection an item is (cached
+// head, column tile); with it (cached head, row, column tile) for the rows that have a position.
+struct Seq {
+  int ctx, n_new, start;   // tokens in the cache, rows of this call, position of row 0
+  int row0, n_rows;        // with selection: first row with a position, and how many
+  int n_list, items, nb;   // keys of an item in list order, number of items, blocks of an item
 };
 
-// Whether row t of the unit's sequence is one of its tokens (padding is answered with zeros).
-__device__ __forceinline__ bool row_live(const Unit& u, int t) { return t < u.n_new && u.start + t >= 0; }
-
-__device__ __forceinline__ Unit unit_of(const AttendArgs& a, int unit) {
-  Unit u;
+__device__ __forceinline__ Seq seq_of(const AttendArgs& a, int b) {
+  Seq s;
+  s.ctx = ctx_of(a.pg, b);
+  s.n_new = new_of(a.pg, b);
+  s.start = s.ctx - s.n_new;
+  s.row0 = s.start < 0 ? -s.start : 0;
+  s.n_rows = max(0, s.n_new - s.row0);
   const bool sel = a.selected != nullptr;
-  u.t = sel ? unit % a.pg.T : 0;
-  const int bh = sel ? unit / a.pg.T : unit;
-  u.b = bh / a.pg.H;
-  u.h = bh - u.b * a.pg.H;
-  u.ctx = ctx_of(a.pg, u.b);
-  u.n_new = new_of(a.pg, u.b);
-  u.start = u.ctx - u.n_new;
-  u.n_list = sel ? a.n_select << a.pg.page_log2 : u.ctx;
-  // no row with a position (the last row's is ctx - 1): nothing to do
-  if (sel ? !row_live(u, u.t) : !(u.n_new > 0 && u.ctx > 0)) u.n_list = 0;
-  return u;
+  if (!sel && s.n_rows > 0) {
+    s.row0 = 0;
+    s.n_rows = 1;
+  }
+  s.n_list = s.n_rows > 0 ? (sel ? a.n_select << a.pg.page_log2 : s.ctx) : 0;
+  s.items = a.pg.H * s.n_rows * a.n_ct;
+  s.nb = (s.n_list + kBlockTiles * kTileTokens - 1) / (kBlockTiles * kTileTokens);
+  return s;
+}
+
+// Whether row t is one of the sequence's tokens (padding is answered with zeros).
+__device__ __forceinline__ bool row_live(const Seq& s, int t) { return t < s.n_new && s.start + t >= 0; }
+
+// Sum of v over the lanes up to and including this one.
+__device__ __forceinline__ long long warp_scan(long long v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+// Blocks of all sequences, and of those before b (whole warp).
+__device__ __forceinline__ void work_before(const AttendArgs& a, int b, int lane, long long& total, long long& before) {
+  total = before = 0;
+  for (int i0 = 0; i0 < a.B; i0 += 32) {
+    long long v = 0;
+    if (i0 + lane < a.B) {
+      const Seq s = seq_of(a, i0 + lane);
+      v = (long long)s.items * s.nb;
+    }
+    const long long sum = warp_scan(v, lane);
+    if (b >= i0 && b < i0 + 32) before = total + __shfl_sync(0xffffffffu, sum - v, b - i0);
+    total += __shfl_sync(0xffffffffu, sum, 31);
+  }
+}
+
+// The sequence that block x of the work belongs to, and the blocks before it (whole warp).
+__device__ __forceinline__ int work_find(const AttendArgs& a, long long x, int lane, long long& before) {
+  before = 0;
+  for (int i0 = 0; i0 < a.B; i0 += 32) {
+    long long v = 0;
+    if (i0 + lane < a.B) {
+      const Seq s = seq_of(a, i0 + lane);
+      v = (long long)s.items * s.nb;
+    }
+    const long long sum = warp_scan(v, lane);
+    const unsigned over = __ballot_sync(0xffffffffu, before + sum > x);
+    if (over) {
+      const int l = __ffs(over) - 1;
+      before += __shfl_sync(0xffffffffu, sum - v, l);
+      return i0 + l;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return a.B;
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -149,6 +204,8 @@ struct AttendCfg {
   static constexpr int kSf = kSt / kTp;          // fragments of a stage
   static constexpr int kQ = CW * NT;             // query columns of a CTA
   static constexpr int kCols = 8 * NT;           // streams of a warp
+  // four tiles fill the time of their own copies with the other warps' work; two take a second stage
+  static constexpr int kStages = kSt > 2 ? 1 : 2;
   static constexpr int kStageBytes = kSt * F::kTile;
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
   static constexpr int kMerge = kAttWarps * kCols * D * 4;
@@ -160,15 +217,22 @@ struct AttendCfg {
   static constexpr int kOffDesc = kOffBar + kAttWarps * kStages * 8;
   static constexpr int kSmem = kOffDesc + kAttWarps * kStages * kSt * 4;
   static_assert(kOffMl % 8 == 0 && kOffBar % 8 == 0 && kOffDesc % 8 == 0, "alignment");
+  static_assert(kBlockTiles % kSt == 0, "blocks are whole stages");
+  // CTAs of an SM: what registers allow (128 threads each) and what shared memory does
+  static constexpr int kByRegs = D == 256 ? 2 : NT == 2 ? (D == 64 ? 3 : 2) : D == 64 ? (kF32 ? 4 : 5)
+                                 : kF32 || GROUP == 32 ? 3 : 4;
+  static constexpr int kBySmem = 227 * 1024 / (kSmem + 1024);
+  static constexpr int kCtas = kByRegs < kBySmem ? kByRegs : kBySmem;
 };
 
 template <typename TQ, int D, int GROUP, int CW, int NT>
-__global__ void __launch_bounds__(kAttThreads)
+__global__ void __launch_bounds__(kAttThreads, AttendCfg<TQ, D, GROUP, CW, NT>::kCtas)
 cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   using F = Fmt<D, GROUP>;
   constexpr int NG = F::kGroups, KS = C::kKs, P = C::kPieces, TP = C::kTp, ST = C::kSt, SF = C::kSf;
   constexpr bool SUB = C::kSub;
+  constexpr int kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int abort_flag;
   uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQ);
@@ -179,33 +243,51 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   int* descs = reinterpret_cast<int*>(smem + C::kOffDesc);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int ct = blockIdx.x % a.n_ct;
-  const long long us = blockIdx.x / a.n_ct;
-  const int unit = (int)(us / a.n_splits), split = (int)(us - (long long)unit * a.n_splits);
-  const Unit u = unit_of(a, unit);
   const bool sel = a.selected != nullptr;
-  const int col0 = ct * C::kQ;
-  const int list0 = split * a.split_tokens;
-  const int list1 = min(u.n_list, list0 + a.split_tokens);
-  if (list0 >= list1 && split > 0) return;  // the first split always answers, with nothing if there is nothing
-
-  // ---- set-up: page entries of the split, query fragments, barriers -------------------------------
   const int pl = a.pg.page_log2;
-  const int32_t* picks = sel ? a.selected + ((long long)(u.b * a.pg.H + u.h) * a.pg.T + u.t) * a.n_select : nullptr;
-  const int e0 = list0 >> pl;
-  const int n_ent = list1 > list0 ? ((list1 - 1) >> pl) - e0 + 1 : 0;
-  for (int i = tid; i < n_ent; i += kAttThreads) {
-    int logical = e0 + i;
-    if (sel) logical = picks[e0 + i];
-    int phys = -1;
-    if (logical >= 0 && logical < a.pg.max_pages && ((long long)logical << pl) < u.ctx) phys = page_of(a.pg, u.b, logical);
-    ent[i] = make_int2(phys, logical << pl);
-  }
+  const uint32_t nibbles = a.nibbles, c128 = a.c128;
+  uint8_t* ring = smem + warp * kStages * C::kStageBytes;
+  uint64_t* bar = bars + warp * kStages;
+  int* desc = descs + warp * kStages * ST;
   if (tid < kAttWarps * kStages) tc::mbar_init(bars + tid, 1);
   if (tid == 0) abort_flag = 0;
-  auto q_row = [&](int col) -> const TQ* {  // the row of a column, or null
-    const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
-    return static_cast<const TQ*>(a.q) + (((long long)u.b * a.pg.H + u.h) * a.G + gg) * (long long)a.pg.T * D +
+  tc::fence_mbar_init();
+  int slot = 0;
+  uint32_t phase = 0;
+
+  // ---- the CTA's stretch of the work -----------------------------------------------------------------
+  long long total, before;
+  work_before(a, 0, lane, total, before);
+  const long long nc = min((long long)a.nc, total);  // CTAs with work: a block each at least
+  if (blockIdx.x >= nc) return;
+  long long x = blockIdx.x * total / nc;
+  const long long x_end = (blockIdx.x + 1) * total / nc;
+  int b = work_find(a, x, lane, before);
+  Seq u = seq_of(a, b);
+
+  while (x < x_end) {
+  while (x >= before + (long long)u.items * u.nb) {  // the next sequence with anything to do
+    before += (long long)u.items * u.nb;
+    u = seq_of(a, ++b);
+  }
+  const int item = (int)((x - before) / u.nb);
+  const int blk0 = (int)((x - before) - (long long)item * u.nb);
+  const int blk1 = (int)min((long long)u.nb, blk0 + (x_end - x));
+  x += blk1 - blk0;
+  const int ct = item % a.n_ct, rest = item / a.n_ct;
+  const int row_t = sel ? u.row0 + rest % u.n_rows : 0;  // the row, with selection
+  const int h = sel ? rest / u.n_rows : rest;
+  const int col0 = ct * C::kQ;
+  const int tile_lo = blk0 * kBlockTiles;
+  const int tile_hi = min(blk1 * kBlockTiles, (u.n_list + kTileTokens - 1) / kTileTokens);
+  tc::fence_proxy_async_smem();  // (the last item's sums lay where copies go now)
+  __syncthreads();
+
+  // ---- set-up of the item: query operands and sums -----------------------------------------------------
+  const int32_t* picks = sel ? a.selected + (((long long)b * a.pg.H + h) * a.pg.T + row_t) * a.n_select : nullptr;
+  auto q_row = [&](int col) -> const TQ* {
+    const int tt = sel ? row_t : col / a.G, gg = sel ? col : col - tt * a.G;
+    return static_cast<const TQ*>(a.q) + (((long long)b * a.pg.H + h) * a.G + gg) * (long long)a.pg.T * D +
            (long long)tt * D;
   };
   // B operands: of fragment column n = i CW + c the query column c, for tile i; zero for the others
@@ -247,7 +329,6 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     for (int o = 1; o < 16 / NG; o <<= 1) x += __shfl_xor_sync(0xffffu << (tid & 16), x, o);
     if (j % (16 / NG) == 0) qs[cc * NG + j / (16 / NG)] = x;
   }
-  tc::fence_mbar_init();
   __syncthreads();
 
   // ---- the lane's streams (C fragment: columns 2 t4 and 2 t4 + 1 of each 8) -------------------------
@@ -260,7 +341,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int col = col0 + nt * CW + (2 * t4 + k) % CW;
-      const int tt = sel ? u.t : col / a.G;
+      const int tt = sel ? row_t : col / a.G;
       const bool live = col < a.cols && row_live(u, tt);
       pos[nt][k] = live ? u.start + tt : -1;
       last[nt][k] = !live ? -1 : (a.causal ? pos[nt][k] : u.ctx - 1);
@@ -318,12 +399,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   }
 
   // ---- the warp's pipeline ------------------------------------------------------------------------
-  const int tile0 = list0 >> 4, tile1 = (list1 + 15) >> 4;  // tiles in list order
-  const int n_stage = list1 > list0 ? (tile1 - tile0 + ST - 1) / ST : 0;
-  uint8_t* ring = smem + warp * kStages * C::kStageBytes;
-  uint64_t* bar = bars + warp * kStages;
-  const uint32_t nibbles = a.nibbles, c128 = a.c128;
-  int* desc = descs + warp * kStages * ST;
+  int tile0 = tile_lo, tile1 = tile_lo, e0 = 0;  // the tiles whose pages are looked up, in list order
   auto issue = [&](int st, int slot) {  // lane 0: copies of stage st, and the positions of its tiles (-1: none)
     uint32_t bytes = 0;
     const uint8_t* src[ST];
@@ -336,7 +412,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         const int2 e = ent[((tile << 4) >> pl) - e0];
         const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
         if (e.x >= 0 && p < u.ctx) {
-          src[k] = a.cache + tile_offset(a.pg, e.x, u.h, p, F::kTile);
+          src[k] = a.cache + tile_offset(a.pg, e.x, h, p, F::kTile);
           bytes += F::kTile;
           first = p;
         }
@@ -353,10 +429,6 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       from = k;
     }
   };
-  if (lane == 0)
-    for (int i = 0; i < kStages; ++i)
-      if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, i);
-
   // One stage of ST tiles.  MASKED: a tile may be missing, and every key is tested against the columns.
   auto consume = [&](const uint8_t* buf, const int* first, auto masked_c) {  // first: positions, in shared memory
     constexpr bool MASKED = decltype(masked_c)::value;
@@ -593,8 +665,28 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     }
   };
 
-  int slot = 0;
-  uint32_t phase = 0;
+  while (tile1 < tile_hi) {
+  // pages of the next tiles (the table and, with selection, the list), as many as are held at a time
+  tile0 = tile1;
+  e0 = (tile0 << 4) >> pl;
+  tile1 = (int)min((long long)tile_hi, ((long long)(e0 + kMaxEntries) << pl) >> 4);
+  const int n_ent = (((tile1 - 1) << 4) >> pl) - e0 + 1;
+  if (tile0 != tile_lo) __syncthreads();
+  for (int i = tid; i < n_ent; i += kAttThreads) {
+    int logical = e0 + i;
+    if (sel) logical = picks[e0 + i];
+    int phys = -1;
+    if (logical >= 0 && logical < a.pg.max_pages && ((long long)logical << pl) < u.ctx) phys = page_of(a.pg, b, logical);
+    ent[i] = make_int2(phys, logical << pl);
+  }
+  __syncthreads();
+  const int n_stage = (tile1 - tile0 + ST - 1) / ST;
+  if (lane == 0)
+    for (int i = 0, s2 = slot; i < kStages; ++i) {
+      if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, s2);
+      s2 = s2 + 1 == kStages ? 0 : s2 + 1;
+    }
+  __syncwarp();
   for (int st = warp; st < n_stage; st += kAttWarps) {
     if (!tc::mbar_wait(bar + slot, phase, &abort_flag)) {
       // give the copies in flight the same time each, then leave
@@ -627,9 +719,9 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       phase ^= 1;
     }
   }
+  }
 
   // ---- join the warps -----------------------------------------------------------------------------
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -664,61 +756,81 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     float mx = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kAttWarps * TP; ++w) mx = fmaxf(mx, ml[w / TP * C::kCols + n0 + w % TP * CW].x);
-    float sum = 0.f, x = 0.f;
+    float sum = 0.f, y = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttWarps * TP; ++w) {
       const int j = w / TP * C::kCols + n0 + w % TP * CW;
       const float2 v = ml[j];
       const float f = v.x == mx ? 1.f : exp2f(v.x - mx);
       sum = fmaf(v.y, f, sum);
-      x = fmaf(om[j * D + d], f, x);
+      y = fmaf(om[j * D + d], f, y);
     }
-    if (a.n_splits == 1) {
-      const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
-      const long long row = (((long long)u.b * a.pg.H + u.h) * a.G + gg) * a.pg.T + tt;
+    if (blk0 == 0 && blk1 == u.nb) {
+      const int tt = sel ? row_t : col / a.G, gg = sel ? col : col - tt * a.G;
+      const long long row = (((long long)b * a.pg.H + h) * a.G + gg) * a.pg.T + tt;
       if (!row_live(u, tt)) sum = 0.f;
-      x = sum == 0.f ? 0.f : x / sum;
+      y = sum == 0.f ? 0.f : y / sum;
       if (a.out_f32)
-        static_cast<float*>(a.out)[row * D + d] = x;
+        static_cast<float*>(a.out)[row * D + d] = y;
       else
-        static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(x);
+        static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(y);
       if (d == 0) a.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
     } else {
-      const long long pi = ((long long)unit * a.n_splits + split) * a.cols + col;
-      a.part_o[pi * D + d] = x;
+      const long long pi = ((long long)blockIdx.x * 2 + (blk0 == 0 ? 1 : 0)) * C::kQ + cc;
+      a.part_o[pi * D + d] = y;
       if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * pi) = make_float2(mx, sum);
     }
   }
+  }
 }
 
-// Joins the splits of a column: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// Joins the pieces of a column: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, and answers the
+// rows that no item has (padding).
 constexpr int kJoinThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttendArgs a) {
-  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;  // 4 dims a thread, the splits dealt out
+  constexpr int kLanes = D / 4, kParts = kJoinThreads / kLanes;  // 4 dims a thread, the pieces dealt out
   __shared__ float4 so[kParts][kLanes];
   __shared__ float2 sml[kParts];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const bool sel = a.selected != nullptr;
   const int unit = blockIdx.x / a.cols, col = blockIdx.x - unit * a.cols;
+  const int bh = sel ? unit / a.pg.T : unit;
+  const int b = bh / a.pg.H, h = bh - b * a.pg.H;
+  const int tt = sel ? unit - bh * a.pg.T : col / a.G, gg = sel ? col : col - tt * a.G;
   const int j = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
-  const Unit u = unit_of(a, unit);
-  const int n = u.n_list > 0 ? (u.n_list + a.split_tokens - 1) / a.split_tokens : 1;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + (long long)unit * a.n_splits * a.cols + col;
-  const float* po = a.part_o + ((long long)unit * a.n_splits * a.cols + col) * D + 4 * j;
+  const Seq u = seq_of(a, b);
   float mx = -INFINITY, sum = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = part; i < n; i += kParts) {
-    const float2 v = ml[(long long)i * a.cols];
-    const float4 y = *reinterpret_cast<const float4*>(po + (long long)i * a.cols * D);
-    const float mn = fmaxf(mx, v.x);
-    const float f = mx == mn ? 1.f : exp2f(mx - mn), e = v.x == mn ? 1.f : exp2f(v.x - mn);
-    mx = mn;
-    sum = sum * f + v.y * e;
-    x.x = x.x * f + y.x * e;
-    x.y = x.y * f + y.y * e;
-    x.z = x.z * f + y.z * e;
-    x.w = x.w * f + y.w * e;
+  const int ct = col / a.tile_cols, cc = col - ct * a.tile_cols;
+  int c0 = 0, c1 = -1;  // the CTAs that have pieces
+  if (u.n_rows > 0 && (!sel || row_live(u, tt))) {
+    long long total, before;
+    work_before(a, b, threadIdx.x & 31, total, before);
+    const long long item = ((sel ? (long long)h * u.n_rows + tt - u.row0 : h) * a.n_ct) + ct;
+    const long long first = before + item * u.nb;
+    // CTA of block y: the largest c with floor(c total / nc) <= y
+    const long long nc = min((long long)a.nc, total);
+    c0 = (int)(((first + 1) * nc - 1) / total);
+    c1 = (int)(((first + u.nb) * nc - 1) / total);
+  }
+  // before any thread leaves: the stream must not go on while the CTAs still write
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;  // written by its CTA
+  {
+    for (int c = c0 + part; c <= c1; c += kParts) {
+      const long long pi = ((long long)c * 2 + (c == c0 ? 1 : 0)) * a.tile_cols + cc;
+      const float2 v = *reinterpret_cast<const float2*>(a.part_ml + 2 * pi);
+      const float4 y = *reinterpret_cast<const float4*>(a.part_o + pi * D + 4 * j);
+      const float mn = fmaxf(mx, v.x);
+      const float f = mx == mn ? 1.f : exp2f(mx - mn), e = v.x == mn ? 1.f : exp2f(v.x - mn);
+      mx = mn;
+      sum = sum * f + v.y * e;
+      x.x = x.x * f + y.x * e;
+      x.y = x.y * f + y.y * e;
+      x.z = x.z * f + y.z * e;
+      x.w = x.w * f + y.w * e;
+    }
   }
   so[part][j] = x;
   if (j == 0) sml[part] = make_float2(mx, sum);
@@ -738,9 +850,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
     r[2] = fmaf(so[i][j].z, f, r[2]);
     r[3] = fmaf(so[i][j].w, f, r[3]);
   }
-  const bool sel = a.selected != nullptr;
-  const int tt = sel ? u.t : col / a.G, gg = sel ? col : col - tt * a.G;
-  const long long row = (((long long)u.b * a.pg.H + u.h) * a.G + gg) * a.pg.T + tt;
+  const long long row = (((long long)b * a.pg.H + h) * a.G + gg) * a.pg.T + tt;
   if (!row_live(u, tt)) sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = sum == 0.f ? 0.f : r[i] / sum;
