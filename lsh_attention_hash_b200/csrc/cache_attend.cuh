@@ -4,24 +4,28 @@
 //
 // With K = z + s c by groups of dims, a query's logit needs only whole codes on the
 // matrix units:  q . K = sum_grp ( s_grp sum_d q_d c_d + z_grp sum_d q_d ),  and
-// the output  O_d = sum_j (p_j s_j) c_jd + sum_j p_j z_j.  So codes 0..15 (exact in
-// bf16) are the A operand of mma.m16n8k16 and the queries (then the weights
-// p_j s_j) its B operand: S^T = K Q^T and O^T = V^T P^T, 8 columns wide.  With keys as
-// the 16 rows, a group of query heads or several new tokens share every key that is
-// unpacked.
+// the output  O_d = sum_j (p_j s_j) c_jd + sum_j p_j z_j.  So codes are the A operand and
+// the queries (then the weights p_j s_j) the B operand: S^T = K Q^T and O^T = V^T P^T,
+// 8 columns wide.  With keys as the 16 rows, a group of query heads or several new tokens
+// share every key that is unpacked.
+//
+// What bounds it after memory is unpacking: integer instructions issue at half rate, so
+// their number per code decides.
+//   K: mma.m16n8k32 of 8-bit integers.  A word's 8 codes are two masks and a shift.  The query
+//      is a fixed-point number of the column's largest |q|: 16 bits (an upper and a lower
+//      byte, two products) for bf16 queries, 24 bits (three) for fp32 ones.  The sums are
+//      exact; the rounding of q is 2^-16 (2^-24) of its largest entry.
+//   V: mma.m16n8k16 in bf16, since weights need a float's range.  0x4300 | c is 128 + c in
+//      bf16; the 128 is taken out by one more product per group with a constant -128 operand,
+//      so a code costs no arithmetic beyond its mask.  In fp32 the weights are three bf16
+//      pieces (24 bits), 128 is subtracted from the codes, and the sums leave the matrix
+//      unit after every stage, so that its accumulation does not show.
 //
 // A single token has one or two query columns, and all that follows the products (scales,
 // exponentials, weights) would be done for 8.  So a fragment's 8 columns are CW query columns
 // of each of TP = 8 / CW tiles: tile i's products use a B operand that is zero outside its
 // own CW columns, and add into the same fragment.  Column n = i CW + c is a stream of its
 // own with its own maximum and sum; the streams are joined with the warps at the end.
-//
-// A code becomes a bf16 by masking: 0x4300 | c is 128 + c.  For bf16 queries the 128 is
-// taken out on the other side: S starts at -128 sum q, and one more product per group
-// with a constant -128 operand gives O's share, so a code costs no arithmetic beyond
-// the mask.  fp32 queries are split into three bf16 pieces (24 bits) and the weights too;
-// there 128 is subtracted from the codes and the sums leave the matrix unit every
-// 32 tokens, so that its accumulation does not show.
 //
 // Every warp is a pipeline of its own: a lane copies ST tiles (cp.async.bulk, codes
 // and parameters together, one copy for tiles that lie side by side) into the warp's ring,
@@ -154,6 +158,22 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Codes (unsigned bytes) times signed (BS) or unsigned bytes.
+template <bool BS>
+__device__ __forceinline__ void imma16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if (BS)
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -195,10 +215,12 @@ struct AttendCfg {
   using F = Fmt<D, GROUP>;
   static_assert(CW == 8 || NT == 1, "more than 8 columns go in whole fragments");
   static constexpr bool kF32 = sizeof(TQ) == 4;
-  static constexpr int kPieces = kF32 ? 3 : 1;
-  // 128 taken out of the codes: always in fp32; at D 256 the -128 products' accumulators would not fit
+  static constexpr int kPieces = kF32 ? 3 : 1;   // bf16 pieces of a weight
+  static constexpr int kBytes = kF32 ? 3 : 2;    // bytes of a query's fixed-point number,
+  static constexpr int kTop = kF32 ? 0x7fffff : 0x7fff;  // and its largest value
+  // 128 taken out of V's codes: always in fp32; at D 256 the -128 products' accumulators would not fit
   static constexpr bool kSub = kF32 || D == 256;
-  static constexpr int kKs = D / 16;             // k steps of Q K^T, m tiles of V^T P^T
+  static constexpr int kKs = D / 16;             // m tiles of V^T P^T
   static constexpr int kTp = 8 / CW;             // tiles of a fragment
   static constexpr int kSt = kTp > 2 ? kTp : 2;  // tiles of a stage
   static constexpr int kSf = kSt / kTp;          // fragments of a stage
@@ -210,8 +232,8 @@ struct AttendCfg {
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
   static constexpr int kMerge = kAttWarps * kCols * D * 4;
   static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kOffQs = kOffQ + kPieces * NT * kTp * kKs * 32 * 8;
-  static constexpr int kOffMl = kOffQs + kQ * F::kGroups * 4;
+  static constexpr int kOffQs = kOffQ + kBytes * NT * kTp * (D / 32) * 32 * 8;
+  static constexpr int kOffMl = kOffQs + kQ * (F::kGroups + 1) * 4;
   static constexpr int kOffEnt = kOffMl + kAttWarps * kCols * 8;
   static constexpr int kOffBar = kOffEnt + kMaxEntries * 8;
   static constexpr int kOffDesc = kOffBar + kAttWarps * kStages * 8;
@@ -237,6 +259,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   __shared__ int abort_flag;
   uint4* qf = reinterpret_cast<uint4*>(smem + C::kOffQ);
   float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
+  float* qstep = qs + C::kQ * NG;
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   int2* ent = reinterpret_cast<int2*>(smem + C::kOffEnt);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
@@ -290,44 +313,60 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     return static_cast<const TQ*>(a.q) + (((long long)b * a.pg.H + h) * a.G + gg) * (long long)a.pg.T * D +
            (long long)tt * D;
   };
-  // B operands: of fragment column n = i CW + c the query column c, for tile i; zero for the others
-  for (int i = tid; i < NT * KS * 32; i += kAttThreads) {
-    const int l = i & 31, ks = (i >> 5) % KS, nt = (i >> 5) / KS;
-    const int n = l >> 2, col = col0 + nt * CW + n % CW;
-    const int d0 = 32 * (ks >> 1) + 8 * (ks & 1) + 2 * (l & 3);
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (col < a.cols) {
-      const TQ* q = q_row(col);
-      x[0] = to_f32<TQ>(q[d0]); x[1] = to_f32<TQ>(q[d0 + 16]);
-      x[2] = to_f32<TQ>(q[d0 + 1]); x[3] = to_f32<TQ>(q[d0 + 17]);
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float y[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        y[k] = __bfloat162float(__float2bfloat16_rn(x[k]));
-        x[k] -= y[k];
-      }
-      const uint2 w = make_uint2(tc::pack_bf16x2(y[0], y[1]), tc::pack_bf16x2(y[2], y[3]));
-#pragma unroll
-      for (int t = 0; t < TP; ++t)
-        reinterpret_cast<uint2*>(qf + (((p * NT + nt) * TP + t) * (KS / 2) + (ks >> 1)) * 32 + l)[ks & 1] =
-            n / CW == t ? w : make_uint2(0, 0);
-    }
-  }
-  // sums of the queries by group: 16 threads a column, D/16 dims each
+  // 16 threads a column: sums by group, and the step of the fixed-point numbers
   for (int cc = tid >> 4; cc < C::kQ; cc += kAttThreads / 16) {
     const int j = tid & 15;
-    float x = 0.f;
+    const uint32_t half = 0xffffu << (tid & 16);
+    float sum = 0.f, top = 0.f;
     if (col0 + cc < a.cols) {
       const TQ* q = q_row(col0 + cc) + j * (D / 16);
 #pragma unroll
-      for (int d = 0; d < D / 16; ++d) x += to_f32<TQ>(q[d]);
+      for (int d = 0; d < D / 16; ++d) {
+        const float v = to_f32<TQ>(q[d]);
+        sum += v;
+        // a NaN counts as infinity: the step is then infinite and so is, or NaN, every logit
+        top = fmaxf(top, v == v ? fabsf(v) : INFINITY);
+      }
     }
 #pragma unroll
-    for (int o = 1; o < 16 / NG; o <<= 1) x += __shfl_xor_sync(0xffffu << (tid & 16), x, o);
-    if (j % (16 / NG) == 0) qs[cc * NG + j / (16 / NG)] = x;
+    for (int o = 1; o < 16; o <<= 1) {
+      if (o < 16 / NG) sum += __shfl_xor_sync(half, sum, o);
+      top = fmaxf(top, __shfl_xor_sync(half, top, o));
+    }
+    if (j % (16 / NG) == 0) qs[cc * NG + j / (16 / NG)] = sum;
+    if (j == 0) qstep[cc] = top / C::kTop;
+  }
+  __syncthreads();
+  // B operands of K's products, byte by byte: fragment column n = i CW + c holds query column c for
+  // tile i and zero for the others; word w covers dims 32 w .. 32 w + 31
+  for (int i = tid; i < NT * (D / 32) * 32; i += kAttThreads) {
+    const int l = i & 31, w = (i >> 5) % (D / 32), nt = (i >> 5) / (D / 32);
+    const int n = l >> 2, cc = nt * CW + n % CW, col = col0 + cc;
+    const float step = qstep[cc];
+    const float inv = step > 0.f ? 1.f / step : 0.f;
+    uint32_t v[C::kBytes][2];
+#pragma unroll
+    for (int p = 0; p < C::kBytes; ++p) v[p][0] = v[p][1] = 0u;
+    if (col < a.cols) {
+      const TQ* q = q_row(col) + 32 * w + 2 * (l & 3);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = to_f32<TQ>(q[8 * k + e]);
+          // x / step; a step too small to invert (denormal queries) is divided by
+          const float y = inv < INFINITY ? x * inv : x / step;
+          const int f = max(-C::kTop, min(C::kTop, __float2int_rn(y)));
+#pragma unroll
+          for (int p = 0; p < C::kBytes; ++p) v[p][e] |= ((f >> (8 * p)) & 255) << (8 * k);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < C::kBytes; ++p)
+#pragma unroll
+      for (int t = 0; t < TP; ++t)
+        reinterpret_cast<uint2*>(qf + (((p * NT + nt) * TP + t) * (D / 64) + (w >> 1)) * 32 + l)[w & 1] =
+            n / CW == t ? make_uint2(v[p][0], v[p][1]) : make_uint2(0u, 0u);
   }
   __syncthreads();
 
@@ -368,13 +407,18 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) fast = min(fast, __shfl_xor_sync(0xffffffffu, fast, o));
 
-  float qsum[NT][NG][2];
+  float qsum[NT][NG][2], step[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) qsum[nt][n][k] = qs[(nt * CW + (2 * t4 + k) % CW) * NG + n];
+
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) step[nt][k] = qstep[nt * CW + (2 * t4 + k) % CW];
 
   float m[NT][2], base[NT][2], bar_m[NT][2], l[NT][2];  // maximum; what is subtracted; where it has to move
   float o[NT][KS][4], zs[NT][NG][2], cb[SUB ? 1 : NT][SUB ? 1 : NG][4];
@@ -436,13 +480,15 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     float s[SF][NT][4];
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
-      float part[NT][NG][4];
+      int part[C::kBytes][NT][NG][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int p = 0; p < C::kBytes; ++p)
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) part[nt][n][c] = SUB ? 0.f : -128.f * qsum[nt][n][c & 1];
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) part[p][nt][n][c] = 0;
 #pragma unroll
       for (int i = 0; i < TP; ++i) {
         const int k = f * TP + i;
@@ -452,23 +498,28 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         lds_words<D / 32>(tb + g * (D / 2) + t4 * (D / 8), wa);
         lds_words<D / 32>(tb + (g + 8) * (D / 2) + t4 * (D / 8), wb);
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {  // two k steps a word
-          const int n = w * 32 / GROUP;
-          uint32_t x[2][4];
+        for (int w = 0; w < D / 32; w += 2) {
+          uint32_t y[2][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            x[e][0] = codes2<SUB>(wa[w], 2 * e, nibbles, c128);
-            x[e][1] = codes2<SUB>(wb[w], 2 * e, nibbles, c128);
-            x[e][2] = codes2<SUB>(wa[w], 2 * e + 1, nibbles, c128);
-            x[e][3] = codes2<SUB>(wb[w], 2 * e + 1, nibbles, c128);
+            y[e][0] = wa[w + e] & 0x0f0f0f0fu;
+            y[e][1] = wb[w + e] & 0x0f0f0f0fu;
+            y[e][2] = (wa[w + e] >> 4) & 0x0f0f0f0fu;
+            y[e][3] = (wb[w + e] >> 4) & 0x0f0f0f0fu;
           }
 #pragma unroll
-          for (int p = P - 1; p >= 0; --p)
+          for (int p = 0; p < C::kBytes; ++p)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint4 b = qf[(((p * NT + nt) * TP + i) * (KS / 2) + w) * 32 + lane];
-              mma16816(part[nt][n], x[0][0], x[0][1], x[0][2], x[0][3], b.x, b.y);
-              mma16816(part[nt][n], x[1][0], x[1][1], x[1][2], x[1][3], b.z, b.w);
+              const uint4 q = qf[(((p * NT + nt) * TP + i) * (D / 64) + w / 2) * 32 + lane];
+              constexpr int kLast = C::kBytes - 1;
+              if (p == kLast) {
+                imma16832<true>(part[p][nt][w * 32 / GROUP], y[0][0], y[0][1], y[0][2], y[0][3], q.x, q.y);
+                imma16832<true>(part[p][nt][(w + 1) * 32 / GROUP], y[1][0], y[1][1], y[1][2], y[1][3], q.z, q.w);
+              } else {
+                imma16832<false>(part[p][nt][w * 32 / GROUP], y[0][0], y[0][1], y[0][2], y[0][3], q.x, q.y);
+                imma16832<false>(part[p][nt][(w + 1) * 32 / GROUP], y[1][0], y[1][1], y[1][2], y[1][3], q.z, q.w);
+              }
             }
         }
       }
@@ -476,11 +527,11 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       const int first_mine = MASKED ? first[mine] : 0;
       const uint8_t* tb = buf + mine * F::kTile;
       const uint32_t* kp = reinterpret_cast<const uint32_t*>(tb + F::kOffKp);
-      float acc[NT][4];
+      float acc[NT][4], zero[NT][4];  // sum of s (codes . q) in steps of q, and of z (sum of q)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
+        for (int c = 0; c < 4; ++c) acc[nt][c] = zero[nt][c] = 0.f;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const uint32_t pa = kp[n * 16 + g], pb = kp[n * 16 + g + 8];
@@ -489,11 +540,19 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            acc[nt][c] = fmaf(sa, part[nt][n][c], fmaf(za, qsum[nt][n][c], acc[nt][c]));
-            acc[nt][2 + c] = fmaf(sb, part[nt][n][2 + c], fmaf(zb, qsum[nt][n][c], acc[nt][2 + c]));
+          for (int c = 0; c < 4; ++c) {
+            // at most 64 * 15 * 2^15 in 16 bits; the third byte joins in float
+            const int v16 = part[C::kBytes - 1][nt][n][c] * 256 + part[C::kBytes - 2][nt][n][c];
+            float v = (float)v16;
+            if (C::kBytes == 3) v = fmaf(v, 256.f, (float)part[0][nt][n][c]);
+            acc[nt][c] = fmaf(c < 2 ? sa : sb, v, acc[nt][c]);
+            zero[nt][c] = fmaf(c < 2 ? za : zb, qsum[nt][n][c & 1], zero[nt][c]);
           }
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[nt][c] = fmaf(acc[nt][c], step[nt][c & 1], zero[nt][c]);
       float fa = a.scale_log2, fb = a.scale_log2;
       if (a.unit_keys) {
         const float* inv = reinterpret_cast<const float*>(tb + F::kOffInv);
