@@ -380,8 +380,8 @@ LSH_API lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int
                                     int mask, int32_t* selected, int32_t* scores, void* stream);
 
 /*
- * Bytes of scratch that lsh_cache_attend needs for these sizes (0 when none); n_select 0
- * without selection.
+ * Bytes of scratch that lsh_cache_attend needs for these sizes (0 for sizes it does not take);
+ * n_select 0 without selection.
  */
 LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, int D, int max_pages, int page,
                                                 int n_select);
@@ -401,13 +401,16 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *   out        [B, Hq, T, D] out_dtype     out: softmax-weighted stored values; 0 for padding
  *                                          and rows without an admissible key
  *   lse        [B, Hq, T] float            out: log-sum-exp of the logits; -inf for those
- *   workspace  device scratch of at least lsh_cache_attend_workspace_bytes(...) bytes,
+ *   workspace  device scratch of at least lsh_cache_attend_workspace_bytes(...) bytes (never 0),
  *              contents undefined on entry and on exit; calls that may overlap on the GPU
  *              (other streams, graphs replayed at the same time) need one each
  *
- * Sums are fp32.  bf16 queries enter the products exactly and the weights are rounded to
- * bf16; fp32 queries and their weights enter as three bf16 pieces (24 bits).
- * lse makes the result joinable with other key sets by lsh_combine_rounds.
+ * The products with the codes are exact integer sums of fixed-point numbers: a query in steps of
+ * its largest entry / 32639 (fp32: / 8355711), a weight in steps of the largest of its 64 keys'
+ * weights / 65535 (fp32: / 8388607).  Everything else is fp32; keys in any order give the same
+ * result only up to rounding, the same call the same bits.
+ * lse makes the result joinable with other key sets by lsh_combine_rounds, where one of
+ * them has a key for the row.
  */
 LSH_API lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int T, int D, const void* cache,
                                     int n_pages, const int32_t* ctx_len, const int32_t* new_len,

@@ -68,11 +68,11 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
   const bool sel = n_select > 0;
   p.units = (long long)B * H * (sel ? T : 1);
   p.cols = sel ? G : G * T;
-  // few columns: several tiles share a fragment (at D 256 two at most: a stage of four would leave an
-  // SM half as many warps)
-  const int least = D == 256 ? 4 : 2;
-  p.cw = p.cols <= 2 ? least : (p.cols <= 4 && (dtype == LSH_BF16 || D == 256)) ? 4 : 8;
-  p.nt = (dtype == LSH_BF16 && D <= 128 && p.cols > 8) ? 2 : 1;
+  // one or two columns: four or two tiles share a fragment; beyond four, fragments side by side (a
+  // cached token is unpacked once for up to 16 columns; at D 256, and in fp32, registers hold 8)
+  const int most = dtype == LSH_F32 || D == 256 ? 2 : 4;
+  p.cw = p.cols >= 3 ? 4 : p.cols == 2 ? 2 : 1;
+  p.nt = p.cols <= 4 ? 1 : p.cols <= 8 ? 2 : most;
   p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
   const long long keys = (long long)(sel ? n_select : max_pages) * page;
   const int block = lsh::cache::kBlockTiles * lsh::cache::kTileTokens;
@@ -289,23 +289,26 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   a.n_ct = p.n_ct;
   a.cols = p.cols;
   a.tile_cols = p.cw * p.nt;
-  a.nibbles = 0x000f000fu;
-  a.c128 = 0x43004300u;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   cudaStream_t s = as_stream(stream);
   return cache_form_dispatch(D, group, [&](auto DC, auto GC) -> lsh_status {
     constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
     using bf = __nv_bfloat16;
-    constexpr int kLeast = DD == 256 ? 4 : 2;
-    if (dtype == LSH_F32)
-      return p.cw == 8 ? launch_cache_attend<float, DD, GG, 8, 1>(a, p, s)
-                       : launch_cache_attend<float, DD, GG, kLeast, 1>(a, p, s);
-    if (p.cw == kLeast) return launch_cache_attend<bf, DD, GG, kLeast, 1>(a, p, s);
-    if constexpr (DD <= 128) {
-      if (p.cw == 4) return launch_cache_attend<bf, DD, GG, 4, 1>(a, p, s);
-      if (p.nt == 2) return launch_cache_attend<bf, DD, GG, 8, 2>(a, p, s);
+#define LSH_CA(TQ)                                                              \
+  do {                                                                          \
+    if (p.cw == 1) return launch_cache_attend<TQ, DD, GG, 1, 1>(a, p, s);       \
+    if (p.cw == 2) return launch_cache_attend<TQ, DD, GG, 2, 1>(a, p, s);       \
+    if (p.nt == 1) return launch_cache_attend<TQ, DD, GG, 4, 1>(a, p, s);       \
+    if (p.nt == 2) return launch_cache_attend<TQ, DD, GG, 4, 2>(a, p, s);       \
+  } while (0)
+    if (dtype == LSH_F32) {
+      LSH_CA(float);
+    } else {
+      LSH_CA(bf);
+      if constexpr (DD <= 128) return launch_cache_attend<bf, DD, GG, 4, 4>(a, p, s);
     }
-    return launch_cache_attend<bf, DD, GG, 8, 1>(a, p, s);
+#undef LSH_CA
+    return LSH_ERR_UNSUPPORTED;
   });
 }
 

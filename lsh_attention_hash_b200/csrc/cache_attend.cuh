@@ -10,21 +10,25 @@
 // share every key that is unpacked.
 //
 // What bounds it after memory is unpacking: integer instructions issue at half rate, so
-// their number per code decides.
-//   K: mma.m16n8k32 of 8-bit integers.  A word's 8 codes are two masks and a shift.  The query
-//      is a fixed-point number of the column's largest |q|: 16 bits (an upper and a lower
-//      byte, two products) for bf16 queries, 24 bits (three) for fp32 ones.  The sums are
-//      exact; the rounding of q is 2^-16 (2^-24) of its largest entry.
-//   V: mma.m16n8k16 in bf16, since weights need a float's range.  0x4300 | c is 128 + c in
-//      bf16; the 128 is taken out by one more product per group with a constant -128 operand,
-//      so a code costs no arithmetic beyond its mask.  In fp32 the weights are three bf16
-//      pieces (24 bits), 128 is subtracted from the codes, and the sums leave the matrix
-//      unit after every stage, so that its accumulation does not show.
+// their number per code decides.  Both products are mma.m16n8k32 of 8-bit integers: a word's 8
+// codes become bytes by two masks and at most one shift (16 codes as bf16 took 15 instructions,
+// as bytes 6 for K and 8 for V, and one product covers twice the depth).
+//   K: the query is a fixed-point number of the column's largest |q|: 16 bits for bf16 queries,
+//      24 for fp32 ones.  The sums are exact; the rounding of q is 2^-16 (2^-24) of its
+//      largest entry.
+//   V: the weights p_j s_j of a stage's 64 keys are fixed-point numbers of the largest of them,
+//      16 bits for bf16 queries and 23 for fp32 ones; the sums go into float accumulators
+//      after every stage.  A scale for each stage and not for the whole sequence: however many
+//      small weights there are, what rounding takes from a stage is at most 64 half steps of its
+//      own largest weight.  The upper nibbles stay where they are (16 c); their scale takes
+//      the 16 out.  An accumulator that starts at 0x4B400000 is, read as a float, 1.5 * 2^23
+//      plus the sum, so the integers become floats by one subtraction.
 //
-// A single token has one or two query columns, and all that follows the products (scales,
-// exponentials, weights) would be done for 8.  So a fragment's 8 columns are CW query columns
-// of each of TP = 8 / CW tiles: tile i's products use a B operand that is zero outside its
-// own CW columns, and add into the same fragment.  Column n = i CW + c is a stream of its
+// A number's two bytes are two columns of the product (fp32's third byte a second product), so a
+// fragment's 8 columns are 4 numbers: CW queries of each of TP = 4 / CW tiles, tile i's
+// products using a B operand that is zero outside its own columns.  A single query thus
+// fills all lanes: lane 4 g + t4 has keys g and g + 8 of tile t4, and scales, exponentials and
+// weights are done once per key and not for 8 columns.  Slot t4 = i CW + c is a stream of its
 // own with its own maximum and sum; the streams are joined with the warps at the end.
 //
 // Every warp is a pipeline of its own: a lane copies ST tiles (cp.async.bulk, codes
@@ -65,7 +69,6 @@ struct AttendArgs {
   int causal, self_mask, unit_keys, out_f32;
   float scale_log2;         // scale * log2(e)
   int nc, n_ct, cols, tile_cols;  // CTAs; column tiles, all columns, columns of a tile
-  uint32_t nibbles, c128;   // 0x000f000f, 0x43004300 (see codes2)
   Pages pg;
 };
 
@@ -144,54 +147,39 @@ __device__ __forceinline__ int work_find(const AttendArgs& a, long long x, int l
   return a.B;
 }
 
+// A page looked up: its block of the item's head (null: missing) and its first position.
+struct __align__(16) Entry {
+  const uint8_t* src;
+  int pos, pad;
+};
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                : "memory");
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Codes (unsigned bytes) times signed (BS) or unsigned bytes.
+// d = (first ? start : d) + codes (unsigned bytes) times signed (BS) or unsigned bytes.
 template <bool BS>
-__device__ __forceinline__ void imma16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
+__device__ __forceinline__ void imma16832(int (&d)[4], bool first, int start, uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  const int c0 = first ? start : d[0], c1 = first ? start : d[1], c2 = first ? start : d[2], c3 = first ? start : d[3];
   if (BS)
     asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "{%10, %11, %12, %13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
   else
     asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        "{%10, %11, %12, %13};"
+        : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1), "r"(c2), "r"(c3));
 }
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Two codes (the low nibbles of both halves of w >> 4 i) as bf16: 128 + c, or c with SUB.  The
-// constants come in as values (kernel arguments): as literals the mask and the exponent would be
-// two instructions, since one instruction holds one literal.
-template <bool SUB>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, int i, uint32_t nibbles, uint32_t c128) {
-  uint32_t x;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w >> (4 * i)), "r"(nibbles), "r"(c128));  // (w & n) | c
-  if (SUB) {
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&c128));
-    x = *reinterpret_cast<uint32_t*>(&r);
-  }
-  return x;
 }
 
 // N consecutive words of shared memory (8 or 16 byte loads).
@@ -209,40 +197,37 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
   }
 }
 
-// CW: query columns of a tile in a fragment (2, 4 or 8); NT: fragments side by side (CW 8 only).
+// CW: queries of a tile in a fragment (1, 2 or 4); NT: fragments side by side (CW 4 only).
 template <typename TQ, int D, int GROUP, int CW, int NT>
 struct AttendCfg {
   using F = Fmt<D, GROUP>;
-  static_assert(CW == 8 || NT == 1, "more than 8 columns go in whole fragments");
+  static_assert(CW == 4 || NT == 1, "more than 4 queries go in whole fragments");
   static constexpr bool kF32 = sizeof(TQ) == 4;
-  static constexpr int kPieces = kF32 ? 3 : 1;   // bf16 pieces of a weight
-  static constexpr int kBytes = kF32 ? 3 : 2;    // bytes of a query's fixed-point number,
-  static constexpr int kTop = kF32 ? 0x7fffff : 0x7fff;  // and its largest value
-  // 128 taken out of V's codes: always in fp32; at D 256 the -128 products' accumulators would not fit
-  static constexpr bool kSub = kF32 || D == 256;
-  static constexpr int kKs = D / 16;             // m tiles of V^T P^T
-  static constexpr int kTp = 8 / CW;             // tiles of a fragment
-  static constexpr int kSt = kTp > 2 ? kTp : 2;  // tiles of a stage
-  static constexpr int kSf = kSt / kTp;          // fragments of a stage
-  static constexpr int kQ = CW * NT;             // query columns of a CTA
-  static constexpr int kCols = 8 * NT;           // streams of a warp
-  // four tiles fill the time of their own copies with the other warps' work; two take a second stage
-  static constexpr int kStages = kSt > 2 ? 1 : 2;
+  static constexpr int kSets = kF32 ? 2 : 1;  // products for the bytes of a number: (upper, lower) columns; (third, none)
+  // a query's largest number (signed bytes: 127 in each) and a weight's (unsigned)
+  static constexpr int kTop = kF32 ? 127 * 65536 + 127 * 256 + 127 : 127 * 256 + 127;
+  static constexpr int kTopW = kF32 ? 0x7fffff : 0xffff;
+  static constexpr int kMt = D / 16;       // m tiles of V^T P^T
+  static constexpr int kTp = 4 / CW;       // tiles of a fragment
+  static constexpr int kSt = 4;            // tiles of a stage
+  static constexpr int kSf = kSt / kTp;    // fragments of a stage
+  static constexpr int kQ = CW * NT;       // query columns of a CTA
+  static constexpr int kStreams = 4 * NT;  // of a warp
+  static constexpr int kStages = 2;
   static constexpr int kStageBytes = kSt * F::kTile;
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
-  static constexpr int kMerge = kAttWarps * kCols * D * 4;
+  static constexpr int kMerge = kAttWarps * kStreams * D * 4;
   static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kOffQs = kOffQ + kBytes * NT * kTp * (D / 32) * 32 * 8;
-  static constexpr int kOffMl = kOffQs + kQ * (F::kGroups + 1) * 4;
-  static constexpr int kOffEnt = kOffMl + kAttWarps * kCols * 8;
-  static constexpr int kOffBar = kOffEnt + kMaxEntries * 8;
-  static constexpr int kOffDesc = kOffBar + kAttWarps * kStages * 8;
-  static constexpr int kSmem = kOffDesc + kAttWarps * kStages * kSt * 4;
-  static_assert(kOffMl % 8 == 0 && kOffBar % 8 == 0 && kOffDesc % 8 == 0, "alignment");
+  static constexpr int kOffQs = kOffQ + kSets * NT * kTp * (D / 32) * 32 * 8;
+  static constexpr int kOffMl = kOffQs + (kQ * (F::kGroups + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kOffEnt = kOffMl + kAttWarps * kStreams * 8;
+  static_assert(kOffEnt % 16 == 0, "16-byte entries");
+  static constexpr int kOffDesc = kOffEnt + kMaxEntries * 16;
+  static constexpr int kOffBar = kOffDesc + kAttWarps * kStages * kSt * 4;
+  static constexpr int kSmem = kOffBar + kAttWarps * kStages * 8;
   static_assert(kBlockTiles % kSt == 0, "blocks are whole stages");
   // CTAs of an SM: what registers allow (128 threads each) and what shared memory does
-  static constexpr int kByRegs = D == 256 ? 2 : NT == 2 ? (D == 64 ? 3 : 2) : D == 64 ? (kF32 ? 4 : 5)
-                                 : kF32 || GROUP == 32 ? 3 : 4;
+  static constexpr int kByRegs = NT == 4 || D == 256 ? 2 : D == 64 ? 4 : 3;
   static constexpr int kBySmem = 227 * 1024 / (kSmem + 1024);
   static constexpr int kCtas = kByRegs < kBySmem ? kByRegs : kBySmem;
 };
@@ -252,8 +237,7 @@ __global__ void __launch_bounds__(kAttThreads, AttendCfg<TQ, D, GROUP, CW, NT>::
 cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   using F = Fmt<D, GROUP>;
-  constexpr int NG = F::kGroups, KS = C::kKs, P = C::kPieces, TP = C::kTp, ST = C::kSt, SF = C::kSf;
-  constexpr bool SUB = C::kSub;
+  constexpr int NG = F::kGroups, MT = C::kMt, SETS = C::kSets, TP = C::kTp, ST = C::kSt, SF = C::kSf;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int abort_flag;
@@ -261,17 +245,16 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   float* qs = reinterpret_cast<float*>(smem + C::kOffQs);
   float* qstep = qs + C::kQ * NG;
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffMl);
-  int2* ent = reinterpret_cast<int2*>(smem + C::kOffEnt);
+  Entry* ent = reinterpret_cast<Entry*>(smem + C::kOffEnt);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
-  int* descs = reinterpret_cast<int*>(smem + C::kOffDesc);
+  int4* descs = reinterpret_cast<int4*>(smem + C::kOffDesc);  // positions of a stage's tiles, -1: missing
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const bool sel = a.selected != nullptr;
   const int pl = a.pg.page_log2;
-  const uint32_t nibbles = a.nibbles, c128 = a.c128;
   uint8_t* ring = smem + warp * kStages * C::kStageBytes;
   uint64_t* bar = bars + warp * kStages;
-  int* desc = descs + warp * kStages * ST;
+  int4* desc = descs + warp * kStages;
   if (tid < kAttWarps * kStages) tc::mbar_init(bars + tid, 1);
   if (tid == 0) abort_flag = 0;
   tc::fence_mbar_init();
@@ -337,163 +320,149 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     if (j == 0) qstep[cc] = top / C::kTop;
   }
   __syncthreads();
-  // B operands of K's products, byte by byte: fragment column n = i CW + c holds query column c for
-  // tile i and zero for the others; word w covers dims 32 w .. 32 w + 31
+  // B operands of K's products: columns 2 k, 2 k + 1 of a fragment are the upper and lower byte (the third
+  // byte and nothing, in the second set) of slot k = i CW + c, that is of query column c for tile i, and
+  // zero for the other tiles; word w covers dims 32 w .. 32 w + 31.  Bytes are signed, so a lower
+  // byte is -128..127 and the rest is rounded to it.
   for (int i = tid; i < NT * (D / 32) * 32; i += kAttThreads) {
     const int l = i & 31, w = (i >> 5) % (D / 32), nt = (i >> 5) / (D / 32);
-    const int n = l >> 2, cc = nt * CW + n % CW, col = col0 + cc;
+    const int k = l >> 3, cc = nt * CW + k % CW, col = col0 + cc;
+    const bool lower = (l >> 2) & 1;
     const float step = qstep[cc];
     const float inv = step > 0.f ? 1.f / step : 0.f;
-    uint32_t v[C::kBytes][2];
+    uint32_t v[SETS][2];
 #pragma unroll
-    for (int p = 0; p < C::kBytes; ++p) v[p][0] = v[p][1] = 0u;
+    for (int p = 0; p < SETS; ++p) v[p][0] = v[p][1] = 0u;
     if (col < a.cols) {
       const TQ* q = q_row(col) + 32 * w + 2 * (l & 3);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = to_f32<TQ>(q[8 * k + e]);
+          const float x = to_f32<TQ>(q[8 * j + e]);
           // x / step; a step too small to invert (denormal queries) is divided by
           const float y = inv < INFINITY ? x * inv : x / step;
-          const int f = max(-C::kTop, min(C::kTop, __float2int_rn(y)));
-#pragma unroll
-          for (int p = 0; p < C::kBytes; ++p) v[p][e] |= ((f >> (8 * p)) & 255) << (8 * k);
+          int f = max(-C::kTop, min(C::kTop, __float2int_rn(y)));
+          if (C::kF32) {
+            const int b0 = (int8_t)f;  // the third byte
+            if (!lower) v[SETS - 1][e] |= (uint32_t)(b0 & 255) << (8 * j);
+            f = (f - b0) >> 8;
+          }
+          const int b1 = (int8_t)f, b2 = (f - b1) >> 8;
+          v[0][e] |= (uint32_t)((lower ? b1 : b2) & 255) << (8 * j);
         }
     }
 #pragma unroll
-    for (int p = 0; p < C::kBytes; ++p)
+    for (int p = 0; p < SETS; ++p)
 #pragma unroll
       for (int t = 0; t < TP; ++t)
         reinterpret_cast<uint2*>(qf + (((p * NT + nt) * TP + t) * (D / 64) + (w >> 1)) * 32 + l)[w & 1] =
-            n / CW == t ? make_uint2(v[p][0], v[p][1]) : make_uint2(0u, 0u);
+            k / CW == t ? make_uint2(v[p][0], v[p][1]) : make_uint2(0u, 0u);
   }
   __syncthreads();
 
-  // ---- the lane's streams (C fragment: columns 2 t4 and 2 t4 + 1 of each 8) -------------------------
-  const int my_tile = 2 * t4 / CW;  // the tile of a fragment that both belong to
-  int pos[NT][2], last[NT][2];  // position; largest admissible position
-  bool self[NT][2];             // whether its own key is masked
+  // ---- the lane's streams: slot t4 of each fragment -----------------------------------------------------
+  const int my_tile = t4 / CW;  // the tile of a fragment that it belongs to
+  int pos[NT], last[NT];        // position; largest admissible position
+  bool self[NT];                // whether its own key is masked
   int fast = u.ctx;             // tiles that end at or below are admissible to every column
+  float qsum[NT][NG], step[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int col = col0 + nt * CW + (2 * t4 + k) % CW;
-      const int tt = sel ? row_t : col / a.G;
-      const bool live = col < a.cols && row_live(u, tt);
-      pos[nt][k] = live ? u.start + tt : -1;
-      last[nt][k] = !live ? -1 : (a.causal ? pos[nt][k] : u.ctx - 1);
-      self[nt][k] = live && a.self_mask;
-      if (live && a.self_mask) {
-        // its own key counts when nothing else is admissible
-        bool other;
-        if (!sel) {
-          other = last[nt][k] > 0;
-        } else {
-          other = false;
-          for (int i = 0; i < a.n_select && !other; ++i) {
-            const int lp = picks[i];
-            if (lp < 0 || lp >= a.pg.max_pages) continue;
-            const long long f = (long long)lp << pl;
-            const long long e = min((long long)last[nt][k], f + (1 << pl) - 1);  // last admissible of the page
-            other = f <= e && (e > f || f != pos[nt][k]);
-          }
+  for (int nt = 0; nt < NT; ++nt) {
+    const int cc = nt * CW + t4 % CW, col = col0 + cc;
+    const int tt = sel ? row_t : col / a.G;
+    const bool live = col < a.cols && row_live(u, tt);
+    pos[nt] = live ? u.start + tt : -1;
+    last[nt] = !live ? -1 : (a.causal ? pos[nt] : u.ctx - 1);
+    self[nt] = live && a.self_mask;
+    if (live && a.self_mask) {
+      // its own key counts when nothing else is admissible
+      bool other;
+      if (!sel) {
+        other = last[nt] > 0;
+      } else {
+        other = false;
+        for (int i = 0; i < a.n_select && !other; ++i) {
+          const int lp = picks[i];
+          if (lp < 0 || lp >= a.pg.max_pages) continue;
+          const long long f = (long long)lp << pl;
+          const long long e = min((long long)last[nt], f + (1 << pl) - 1);  // last admissible of the page
+          other = f <= e && (e > f || f != pos[nt]);
         }
-        self[nt][k] = other;
       }
-      if (live && (a.causal || a.self_mask)) fast = min(fast, pos[nt][k]);
+      self[nt] = other;
     }
+    if (live && (a.causal || a.self_mask)) fast = min(fast, pos[nt]);
+    step[nt] = qstep[cc];
+#pragma unroll
+    for (int n = 0; n < NG; ++n) qsum[nt][n] = qs[cc * NG + n];
+  }
 #pragma unroll
   for (int o = 1; o < 4; o <<= 1) fast = min(fast, __shfl_xor_sync(0xffffffffu, fast, o));
 
-  float qsum[NT][NG][2], step[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) qsum[nt][n][k] = qs[(nt * CW + (2 * t4 + k) % CW) * NG + n];
-
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) step[nt][k] = qstep[nt * CW + (2 * t4 + k) % CW];
-
-  float m[NT][2], base[NT][2], bar_m[NT][2], l[NT][2];  // maximum; what is subtracted; where it has to move
-  float o[NT][KS][4], zs[NT][NG][2], cb[SUB ? 1 : NT][SUB ? 1 : NG][4];
+  float m[NT], base[NT], bar_m[NT], l[NT];  // maximum; what is subtracted; where it has to move; sum
+  float o[NT][MT][2], zs[NT][NG];           // dims 16 i + g, + 8; sums of p z
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    m[nt] = bar_m[nt] = -INFINITY;
+    base[nt] = l[nt] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      m[nt][k] = bar_m[nt][k] = -INFINITY;
-      base[nt][k] = l[nt][k] = 0.f;
-    }
+    for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[nt][i][k] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      zs[nt][n][0] = zs[nt][n][1] = 0.f;
-      if (!SUB)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) cb[SUB ? 0 : nt][SUB ? 0 : n][k] = 0.f;
-    }
+    for (int n = 0; n < NG; ++n) zs[nt][n] = 0.f;
   }
 
   // ---- the warp's pipeline ------------------------------------------------------------------------
   int tile0 = tile_lo, tile1 = tile_lo, e0 = 0;  // the tiles whose pages are looked up, in list order
-  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st, and the positions of its tiles (-1: none)
-    uint32_t bytes = 0;
+  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st
+    const int tile = tile0 + st * ST;
+    const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
+    if (pl >= 6) {  // a stage lies inside a page
+      const Entry e = ent[((tile << 4) >> pl) - e0];
+      const int in_page = tile & ((1 << (pl - 4)) - 1);
+      const int p = e.pos + (in_page << 4);
+      // tiles that hold tokens of the sequence (in list order the sequence may end before the list)
+      const int n = e.src ? min(min(ST, tile1 - tile), max(0, (u.ctx - p + kTileTokens - 1) >> 4)) : 0;
+      desc[slot] = make_int4(n > 0 ? p : -1, n > 1 ? p + 16 : -1, n > 2 ? p + 32 : -1, n > 3 ? p + 48 : -1);
+      tc::mbar_arrive_expect_tx(bar + slot, n * F::kTile);
+      if (n > 0) bulk_load(dst, e.src + in_page * F::kTile, n * F::kTile, bar + slot);
+      return;
+    }
     const uint8_t* src[ST];
+    int first[ST];
+    uint32_t bytes = 0;
 #pragma unroll
     for (int k = 0; k < ST; ++k) {
-      const int tile = tile0 + st * ST + k;
       src[k] = nullptr;
-      int first = -1;
-      if (tile < tile1) {
-        const int2 e = ent[((tile << 4) >> pl) - e0];
-        const int p = e.y + ((tile << 4) & ((1 << pl) - 1));
-        if (e.x >= 0 && p < u.ctx) {
-          src[k] = a.cache + tile_offset(a.pg, e.x, h, p, F::kTile);
+      first[k] = -1;
+      if (tile + k < tile1) {
+        const Entry e = ent[(((tile + k) << 4) >> pl) - e0];
+        const int in_page = (tile + k) & ((1 << (pl - 4)) - 1);
+        const int p = e.pos + (in_page << 4);
+        if (e.src && p < u.ctx) {
+          src[k] = e.src + in_page * F::kTile;
+          first[k] = p;
           bytes += F::kTile;
-          first = p;
         }
       }
-      desc[slot * ST + k] = first;
     }
+    desc[slot] = make_int4(first[0], first[1], first[2], first[3]);
     tc::mbar_arrive_expect_tx(bar + slot, bytes);
-    const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
-    int from = 0;  // runs of tiles side by side
 #pragma unroll
-    for (int k = 1; k <= ST; ++k) {
-      if (k < ST && src[k] && src[k] == src[k - 1] + F::kTile) continue;
-      if (src[k - 1]) bulk_load(dst + from * F::kTile, src[k - 1] - (k - 1 - from) * F::kTile, (k - from) * F::kTile, bar + slot);
-      from = k;
-    }
+    for (int k = 0; k < ST; ++k)
+      if (src[k]) bulk_load(dst + k * F::kTile, src[k], F::kTile, bar + slot);
   };
   // One stage of ST tiles.  MASKED: a tile may be missing, and every key is tested against the columns.
   auto consume = [&](const uint8_t* buf, const int* first, auto masked_c) {  // first: positions, in shared memory
     constexpr bool MASKED = decltype(masked_c)::value;
-    // ---- logits: s[f][nt][0,1]: key g of the lane's tile, columns 2 t4, +1;  [2,3]: key g + 8
-    float s[SF][NT][4];
+    // ---- logits of keys g and g + 8 of the lane's tile
+    float s[SF][NT][2];
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
-      int part[C::kBytes][NT][NG][4];
-#pragma unroll
-      for (int p = 0; p < C::kBytes; ++p)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) part[p][nt][n][c] = 0;
+      int part[SETS][NT][NG][4];
 #pragma unroll
       for (int i = 0; i < TP; ++i) {
-        const int k = f * TP + i;
-        if (MASKED && first[k] < 0) continue;
-        const uint8_t* tb = buf + k * F::kTile;
+        const uint8_t* tb = buf + (f * TP + i) * F::kTile;  // (a missing tile's sums are replaced below)
         uint32_t wa[D / 32], wb[D / 32];
         lds_words<D / 32>(tb + g * (D / 2) + t4 * (D / 8), wa);
         lds_words<D / 32>(tb + (g + 8) * (D / 2) + t4 * (D / 8), wb);
@@ -508,17 +477,16 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
             y[e][3] = (wb[w + e] >> 4) & 0x0f0f0f0fu;
           }
 #pragma unroll
-          for (int p = 0; p < C::kBytes; ++p)
+          for (int p = 0; p < SETS; ++p)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 q = qf[(((p * NT + nt) * TP + i) * (D / 64) + w / 2) * 32 + lane];
-              constexpr int kLast = C::kBytes - 1;
-              if (p == kLast) {
-                imma16832<true>(part[p][nt][w * 32 / GROUP], y[0][0], y[0][1], y[0][2], y[0][3], q.x, q.y);
-                imma16832<true>(part[p][nt][(w + 1) * 32 / GROUP], y[1][0], y[1][1], y[1][2], y[1][3], q.z, q.w);
-              } else {
-                imma16832<false>(part[p][nt][w * 32 / GROUP], y[0][0], y[0][1], y[0][2], y[0][3], q.x, q.y);
-                imma16832<false>(part[p][nt][(w + 1) * 32 / GROUP], y[1][0], y[1][1], y[1][2], y[1][3], q.z, q.w);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int n = (w + e) * 32 / GROUP;
+                const bool fresh = i == 0 && (w + e) * 32 % GROUP == 0;
+                imma16832<true>(part[p][nt][n], fresh, 0, y[e][0], y[e][1], y[e][2], y[e][3],
+                                e ? q.z : q.x, e ? q.w : q.y);
               }
             }
         }
@@ -527,200 +495,179 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       const int first_mine = MASKED ? first[mine] : 0;
       const uint8_t* tb = buf + mine * F::kTile;
       const uint32_t* kp = reinterpret_cast<const uint32_t*>(tb + F::kOffKp);
-      float acc[NT][4], zero[NT][4];  // sum of s (codes . q) in steps of q, and of z (sum of q)
+      float acc[NT][2], zero[NT][2];  // sum of s (codes . q) in steps of q, and of z (sum of q)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = zero[nt][0] = zero[nt][1] = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[nt][c] = zero[nt][c] = 0.f;
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const uint32_t pa = kp[n * 16 + g], pb = kp[n * 16 + g + 8];
-        const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
-        const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t pw = kp[n * 16 + g + 8 * r];
+          const float sc = bf16_bits(pw), ze = __uint_as_float(pw & 0xffff0000u);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // at most 64 * 15 * 2^15 in 16 bits; the third byte joins in float
-            const int v16 = part[C::kBytes - 1][nt][n][c] * 256 + part[C::kBytes - 2][nt][n][c];
-            float v = (float)v16;
-            if (C::kBytes == 3) v = fmaf(v, 256.f, (float)part[0][nt][n][c]);
-            acc[nt][c] = fmaf(c < 2 ? sa : sb, v, acc[nt][c]);
-            zero[nt][c] = fmaf(c < 2 ? za : zb, qsum[nt][n][c & 1], zero[nt][c]);
+          for (int nt = 0; nt < NT; ++nt) {
+            // at most 64 * 15 * 2^15; the third byte joins in float
+            float v = (float)(part[0][nt][n][2 * r] * 256 + part[0][nt][n][2 * r + 1]);
+            if (SETS == 2) v = fmaf(v, 256.f, (float)part[SETS - 1][nt][n][2 * r]);
+            acc[nt][r] = fmaf(sc, v, acc[nt][r]);
+            zero[nt][r] = fmaf(ze, qsum[nt][n], zero[nt][r]);
           }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[nt][c] = fmaf(acc[nt][c], step[nt][c & 1], zero[nt][c]);
-      float fa = a.scale_log2, fb = a.scale_log2;
-      if (a.unit_keys) {
-        const float* inv = reinterpret_cast<const float*>(tb + F::kOffInv);
-        fa *= inv[g];
-        fb *= inv[g + 8];
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x = acc[nt][c] * (c < 2 ? fa : fb);
-          if (MASKED) {
-            const int key = first_mine + g + (c < 2 ? 0 : 8);
-            if (first_mine < 0 || key > last[nt][c & 1] || (key == pos[nt][c & 1] && self[nt][c & 1])) x = -INFINITY;
-          }
-          s[f][nt][c] = x;
         }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float fk = a.scale_log2;
+        if (a.unit_keys) fk *= reinterpret_cast<const float*>(tb + F::kOffInv)[g + 8 * r];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x = fmaf(acc[nt][r], step[nt], zero[nt][r]) * fk;
+          if (MASKED) {
+            const int key = first_mine + g + 8 * r;
+            if (first_mine < 0 || key > last[nt] || (key == pos[nt] && self[nt])) x = -INFINITY;
+          }
+          s[f][nt][r] = x;
+        }
+      }
     }
     // ---- the running maximum, moved only when a logit is 2^8 above it
-    float top[NT][2];
+    float top[NT];
     bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float x = fmaxf(s[0][nt][0], s[0][nt][1]);
+#pragma unroll
+      for (int f = 1; f < SF; ++f) x = fmaxf(fmaxf(x, s[f][nt][0]), s[f][nt][1]);
+      top[nt] = x;
+      raise |= x > bar_m[nt];
+    }
+    if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float x = top[nt];
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        const float mn = fmaxf(m[nt], x);
+        const float al = m[nt] == mn ? 1.f : exp2f(m[nt] - mn);
+        m[nt] = mn;
+        base[nt] = mn == -INFINITY ? 0.f : mn;
+        bar_m[nt] = mn == -INFINITY ? mn : mn + kLazyMax;
+        l[nt] *= al;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          o[nt][i][0] *= al;
+          o[nt][i][1] *= al;
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) zs[nt][n] *= al;
+      }
+    }
+    // ---- weights p s: their largest of the stage, then fixed-point numbers of it
+    float wt[SF][NT][NG][2];
+    uint32_t top_w[NT][NG];  // bits of a float that is not negative order as integers do, NaN above all
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-#pragma unroll
-        for (int f = 1; f < SF; ++f) x = fmaxf(fmaxf(x, s[f][nt][c]), s[f][nt][c + 2]);
-        top[nt][c] = x;
-        raise |= x > bar_m[nt][c];
-      }
-    if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x = top[nt][c];
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mn = fmaxf(m[nt][c], x);
-          const float al = m[nt][c] == mn ? 1.f : exp2f(m[nt][c] - mn);
-          m[nt][c] = mn;
-          base[nt][c] = mn == -INFINITY ? 0.f : mn;
-          bar_m[nt][c] = mn == -INFINITY ? mn : mn + kLazyMax;
-          l[nt][c] *= al;
-#pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            o[nt][i][c] *= al;
-            o[nt][i][c + 2] *= al;
-          }
-#pragma unroll
-          for (int n = 0; n < NG; ++n) {
-            zs[nt][n][c] *= al;
-            if (!SUB) {
-              cb[SUB ? 0 : nt][SUB ? 0 : n][c] *= al;
-              cb[SUB ? 0 : nt][SUB ? 0 : n][c + 2] *= al;
-            }
-          }
-        }
-    }
-    float fresh[P > 1 ? NT : 1][P > 1 ? KS : 1][4];  // fp32: this stage's sums
-    if (P > 1) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c] = 0.f;
-    }
+      for (int n = 0; n < NG; ++n) top_w[nt][n] = 0u;
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
-      float p[NT][4];
+      float p[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float x = s[f][nt][c] - base[nt][c & 1];
-          p[nt][c] = P > 1 ? exp2f(x) : tc::ex2_approx(x);
-          l[nt][c & 1] += p[nt][c];
+        for (int r = 0; r < 2; ++r) {
+          const float y = s[f][nt][r] - base[nt];
+          p[nt][r] = C::kF32 ? exp2f(y) : tc::ex2_approx(y);
+          l[nt] += p[nt][r];
         }
       const uint32_t* vp = reinterpret_cast<const uint32_t*>(buf + (f * TP + my_tile) * F::kTile + F::kOffVp);
-      uint32_t pf[P][NG][NT][2];  // B fragments of (p s): [0] keys 0..7, [1] keys 8..15 of every column's tile
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint32_t pw = vp[n * 16 + g + 8 * r];
+          const float sc = bf16_bits(pw), ze = __uint_as_float(pw & 0xffff0000u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const bool out = MASKED && s[f][nt][r] == -INFINITY;  // whatever lies in a masked place
+            const float w = out ? 0.f : p[nt][r] * sc;
+            if (!out) zs[nt][n] = fmaf(p[nt][r], ze, zs[nt][n]);
+            wt[f][nt][n][r] = w;
+            top_w[nt][n] = max(top_w[nt][n], __float_as_uint(w));
+          }
+        }
+    }
+    float unit[NT][NG];                // what a step of the weights is worth
+    uint32_t pb[SF][NT][NG][SETS];     // their bytes in column g: keys 2 t4, +1, 2 t4 + 8, +9 of the column's tile
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const uint32_t pa = vp[n * 16 + g], pb = vp[n * 16 + g + 8];
-        const float sa = bf16_bits(pa), za = __uint_as_float(pa & 0xffff0000u);
-        const float sb = bf16_bits(pb), zb = __uint_as_float(pb & 0xffff0000u);
+        uint32_t t = top_w[nt][n];
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
+        t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
+        const float wm = __uint_as_float(t);
+        unit[nt][n] = wm * (1.f / C::kTopW);
+        // weights below 2^-110 are nothing (a value's scale is 2^-100 at least); NaN and infinity stay
+        // in the unit
+        const float inv = wm > 7.7037197775489434e-34f ? __fdividef((float)C::kTopW, wm) : 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+        for (int f = 0; f < SF; ++f) {
+          uint32_t x[2];  // the number in the low bits of a float's mantissa
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const bool out = MASKED && s[f][nt][c] == -INFINITY;  // whatever lies in a masked place
-            w[c] = out ? 0.f : p[nt][c] * (c < 2 ? sa : sb);
-            if (!out) zs[nt][n][c & 1] = fmaf(p[nt][c], c < 2 ? za : zb, zs[nt][n][c & 1]);
+          for (int r = 0; r < 2; ++r) x[r] = __float_as_uint(fmaf(wt[f][nt][n][r], inv, 8388608.f));
+          // a number's bytes as the two columns of its slot
+#pragma unroll
+          for (int e = 0; e < SETS; ++e) {
+            const uint32_t pick = SETS == 1 ? 0x4041 : e == 0 ? 0x4142 : 0x4440;
+            const uint32_t lo = movmatrix(__byte_perm(x[0], 0u, pick)), hi = movmatrix(__byte_perm(x[1], 0u, pick));
+            pb[f][nt][n][e] = __byte_perm(lo, hi, 0x6420);
           }
+        }
+      }
+    // ---- O += weights . codes, 16 dims of 64 keys at a time
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const uint32_t lo = tc::pack_bf16x2(w[0], w[1]), hi = tc::pack_bf16x2(w[2], w[3]);
-            pf[i][n][nt][0] = movmatrix(lo);
-            pf[i][n][nt][1] = movmatrix(hi);
-            if (i + 1 < P) {
-              w[0] -= bf16_bits(lo); w[1] -= __uint_as_float(lo & 0xffff0000u);
-              w[2] -= bf16_bits(hi); w[3] -= __uint_as_float(hi & 0xffff0000u);
+    for (int q = 0; q < D / 64; ++q) {
+      uint32_t by[ST][4];  // byte j of the four keys of a lane: dims 16 j + g (low nibble), 16 j + 8 + g
+#pragma unroll
+      for (int k = 0; k < ST; ++k) {
+        const uint8_t* vrow = buf + k * F::kTile + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8) + 8 * q;
+        const uint2 u0 = *reinterpret_cast<const uint2*>(vrow), u1 = *reinterpret_cast<const uint2*>(vrow + 4 * D);
+        const uint32_t a01 = __byte_perm(u0.x, u0.y, 0x5140), b01 = __byte_perm(u1.x, u1.y, 0x5140);
+        const uint32_t a23 = __byte_perm(u0.x, u0.y, 0x7362), b23 = __byte_perm(u1.x, u1.y, 0x7362);
+        by[k][0] = __byte_perm(a01, b01, 0x5410);
+        by[k][1] = __byte_perm(a01, b01, 0x7632);
+        by[k][2] = __byte_perm(a23, b23, 0x5410);
+        by[k][3] = __byte_perm(a23, b23, 0x7632);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int mt = 4 * q + j, n = mt * 16 / GROUP;
+        int sum[SETS][NT][4];
+#pragma unroll
+        for (int k = 0; k < ST; k += 2) {  // two tiles: the depth of a product
+          const uint32_t a0 = by[k][j] & 0x0f0f0f0fu, a1 = by[k][j] & 0xf0f0f0f0u;
+          const uint32_t a2 = by[k + 1][j] & 0x0f0f0f0fu, a3 = by[k + 1][j] & 0xf0f0f0f0u;
+#pragma unroll
+          for (int e = 0; e < SETS; ++e)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              // a tile's own columns only
+              const uint32_t b0 = TP == 1 || (g >> 1) / CW == k % TP ? pb[k / TP][nt][n][e] : 0u;
+              const uint32_t b1 = TP == 1 || (g >> 1) / CW == (k + 1) % TP ? pb[(k + 1) / TP][nt][n][e] : 0u;
+              imma16832<false>(sum[e][nt], k == 0, 0x4B400000, a0, a1, a2, a3, b0, b1);
             }
-          }
         }
-      }
-      if (!SUB) {
-        const uint32_t c = 0xc300c300u;  // -128 twice
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(cb[SUB ? 0 : nt][SUB ? 0 : n], c, c, c, c, pf[0][n][nt][0], pf[0][n][nt][1]);
-      }
-#pragma unroll
-      for (int i = 0; i < TP; ++i) {
-        const int k = f * TP + i;
-        if (MASKED && first[k] < 0) continue;
-        const uint8_t* tb = buf + k * F::kTile;
-        uint32_t pb[P][NG][NT][2];  // the tile's own columns
-#pragma unroll
-        for (int pc = 0; pc < P; ++pc)
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) pb[pc][n][nt][e] = TP == 1 || g / CW == i ? pf[pc][n][nt][e] : 0u;
-        const uint8_t* vrow = tb + F::kOffV + t4 * D + (g ^ (2 * t4)) * (D / 8);
-        uint32_t w0[D / 32], w1[D / 32];  // token pairs t4 and t4 + 4
-        lds_words<D / 32>(vrow, w0);
-        lds_words<D / 32>(vrow + 4 * D, w1);
-#pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          // the two tokens of a pair side by side: 16 dims in two words
-          uint32_t r0[2], r1[2];
-          r0[0] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x5410);
-          r0[1] = __byte_perm(w0[2 * q], w0[2 * q + 1], 0x7632);
-          r1[0] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x5410);
-          r1[1] = __byte_perm(w1[2 * q], w1[2 * q + 1], 0x7632);
-#pragma unroll
-          for (int mm = 0; mm < 4; ++mm) {
-            const int mt = 4 * q + mm, n = mt * 16 / GROUP, x = (mm & 1) * 2;
-            const uint32_t a0 = codes2<SUB>(r0[mm >> 1], x, nibbles, c128);
-            const uint32_t a1 = codes2<SUB>(r0[mm >> 1], x + 1, nibbles, c128);
-            const uint32_t a2 = codes2<SUB>(r1[mm >> 1], x, nibbles, c128);
-            const uint32_t a3 = codes2<SUB>(r1[mm >> 1], x + 1, nibbles, c128);
-#pragma unroll
-            for (int pc = P - 1; pc >= 0; --pc)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                float(&dst)[4] = P > 1 ? fresh[P > 1 ? nt : 0][P > 1 ? mt : 0] : o[nt][mt];
-                mma16816(dst, a0, a1, a2, a3, pb[pc][n][nt][0], pb[pc][n][nt][1]);
-              }
+          for (int r = 0; r < 2; ++r) {
+            float v = fmaf(__int_as_float(sum[0][nt][2 * r]) - 12582912.f, 256.f,
+                           __int_as_float(sum[0][nt][2 * r + 1]) - 12582912.f);
+            if (SETS == 2) v = fmaf(v, 256.f, __int_as_float(sum[SETS - 1][nt][2 * r]) - 12582912.f);
+            o[nt][mt][r] = fmaf(v, unit[nt][n] * (r ? 0.0625f : 1.f), o[nt][mt][r]);  // upper nibbles: 16 c
           }
-        }
       }
-    }
-    if (P > 1) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[nt][i][c] += fresh[P > 1 ? nt : 0][P > 1 ? i : 0][c];
     }
   };
 
@@ -736,7 +683,11 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     if (sel) logical = picks[e0 + i];
     int phys = -1;
     if (logical >= 0 && logical < a.pg.max_pages && ((long long)logical << pl) < u.ctx) phys = page_of(a.pg, b, logical);
-    ent[i] = make_int2(phys, logical << pl);
+    Entry e;
+    e.src = phys >= 0 ? a.cache + tile_offset(a.pg, phys, h, 0, F::kTile) : nullptr;
+    e.pos = logical << pl;
+    e.pad = 0;
+    ent[i] = e;
   }
   __syncthreads();
   const int n_stage = (tile1 - tile0 + ST - 1) / ST;
@@ -759,13 +710,9 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       }
       break;
     }
-    const int* first = desc + slot * ST;
-    int lo = first[0], hi = lo;
-#pragma unroll
-    for (int k = 1; k < ST; ++k) {
-      lo = min(lo, first[k]);
-      hi = max(hi, first[k]);
-    }
+    const int4 at = desc[slot];
+    const int* first = reinterpret_cast<const int*>(desc + slot);
+    const int lo = min(min(at.x, at.y), min(at.z, at.w)), hi = max(max(at.x, at.y), max(at.z, at.w));
     const uint8_t* buf = ring + slot * C::kStageBytes;
     if (lo >= 0 && hi + kTileTokens <= fast)
       consume(buf, first, std::false_type());
@@ -782,43 +729,36 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 
   // ---- join the warps -----------------------------------------------------------------------------
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int y = 4; y < 32; y <<= 1) {
+      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], y);
 #pragma unroll
-      for (int x = 4; x < 32; x <<= 1) {
-        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
-#pragma unroll
-        for (int n = 0; n < NG; ++n) zs[nt][n][c] += __shfl_xor_sync(0xffffffffu, zs[nt][n][c], x);
-      }
-      if (g == 0) ml[warp * C::kCols + nt * 8 + 2 * t4 + c] = make_float2(m[nt][c], l[nt][c]);
+      for (int n = 0; n < NG; ++n) zs[nt][n] += __shfl_xor_sync(0xffffffffu, zs[nt][n], y);
     }
+    if (g == 0) ml[warp * C::kStreams + nt * 4 + t4] = make_float2(m[nt], l[nt]);
+  }
   __syncthreads();  // the ring is free
-  float* om = reinterpret_cast<float*>(smem);  // [warp][col][D]
+  float* om = reinterpret_cast<float*>(smem);  // [warp][stream][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      const int n = i * 16 / GROUP;
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float x = o[nt][i][c] + zs[nt][n][c & 1];
-        if (!SUB) x += cb[SUB ? 0 : nt][SUB ? 0 : n][c];
-        om[(warp * C::kCols + nt * 8 + 2 * t4 + (c & 1)) * D + i * 16 + g + (c < 2 ? 0 : 8)] = x;
-      }
-    }
+      for (int r = 0; r < 2; ++r)
+        om[(warp * C::kStreams + nt * 4 + t4) * D + i * 16 + g + 8 * r] = o[nt][i][r] + zs[nt][i * 16 / GROUP];
   __syncthreads();
   for (int i = tid; i < C::kQ * D; i += kAttThreads) {
     const int cc = i / D, d = i - cc * D, col = col0 + cc;
     if (col >= a.cols) break;
-    const int n0 = NT > 1 ? cc : cc % CW;  // its first stream; the others CW further each
+    // its streams: slot cc of every warp, and CW further for each other tile of a fragment
     float mx = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kAttWarps * TP; ++w) mx = fmaxf(mx, ml[w / TP * C::kCols + n0 + w % TP * CW].x);
+    for (int w = 0; w < kAttWarps * TP; ++w) mx = fmaxf(mx, ml[w / TP * C::kStreams + cc + w % TP * CW].x);
     float sum = 0.f, y = 0.f;
 #pragma unroll
     for (int w = 0; w < kAttWarps * TP; ++w) {
-      const int j = w / TP * C::kCols + n0 + w % TP * CW;
+      const int j = w / TP * C::kStreams + cc + w % TP * CW;
       const float2 v = ml[j];
       const float f = v.x == mx ? 1.f : exp2f(v.x - mx);
       sum = fmaf(v.y, f, sum);

@@ -212,23 +212,21 @@ def test_write_bad_pages_and_lengths_are_skipped():
 # ---------------------------------------------------------------------------------------------------
 # Attention
 
-def _bounds(q, V, zV, K_scale, w, D, group, scale, f32_in, f32_out, want):
-    """Bound of the output's error per dim, and of the lse's.
+def _bounds(q, K, zK, V, zV, sV, w, key_scale, f32_in, f32_out, want):
+    """Bound of the output's error per dim, and of the lse's, from the roundings that the kernel states.
 
-    Logit: per group the codes' sum is added up on the matrix unit in GROUP/16 steps (three pieces each
-    in fp32), each step off by at most 2^-22 of the largest partial sum; codes are 143 at most while
-    the 128 is in them (bf16), else 15.  Weights p s go in as bf16 (2^-8 half a step for bf16's 8 bits) or
-    in three pieces (2^-24); exp2 and the other float steps 2^-20.  l adds the unrounded weights.
+    Logit of key j: the code part sum_d q_d (K - z)_jd takes q rounded to half a step, step = max|q| / 32639
+    (fp32: / 8355711); the integer sums are exact; what float does to the code part and to z's part is
+    within 2^-20 of their sizes.  Weights p s go in as fixed-point numbers of the largest of their stage:
+    half a step, 1 / 65535 (fp32: 1 / 8388607) of it, times codes of at most 15; the largest of any stage is
+    at most the largest of all.  exp2 and the other float steps are within 2^-18 of the sizes.
     """
-    steps = group // 16 * (3 if f32_in else 1)
-    top = 15.0 if f32_in else 143.0
-    dz = steps * 2.0 ** -22 * top * np.abs(q).sum() * K_scale * scale + 2.0 ** -20
-    wr = 2.0 ** -24 if f32_in else 2.0 ** -8
-    codes = w @ np.abs(V - zV)          # the part that goes through the rounded weights
-    size = w @ (np.abs(V - zV) * (1 if f32_in else 143.0 / 7.5) + np.abs(zV)) if w.size else 0.0
-    out = wr * codes + (2 * dz + 2.0 ** -17) * (w @ np.abs(V)) + 2.0 ** -20 * size
-    out = out + np.abs(want) * (2.0 ** -24 if f32_out else 2.0 ** -8)
-    return out, dz + 2.0 ** -19
+    step = np.abs(q).max() / (8355711 if f32_in else 32639)
+    code = np.abs(K - zK)
+    dz = ((0.5 * step * code.sum(1) + 2.0 ** -20 * ((code + np.abs(zK)) @ np.abs(q))) * key_scale).max() + 2.0 ** -20
+    unit = (w[:, None] * sV).max(0) / (8388607 if f32_in else 65535)
+    out = w.size * 7.5 * unit + (2 * dz + 2.0 ** -18) * (w @ (np.abs(V - zV) + np.abs(zV)))
+    return out + np.abs(want) * (2.0 ** -24 if f32_out else 2.0 ** -8), dz + 2.0 ** -18
 
 
 def _check_attend(c, q, out, lse, new, selected=None, self_mask=True, causal=True, unit_keys=True, scale=None):
@@ -241,9 +239,9 @@ def _check_attend(c, q, out, lse, new, selected=None, self_mask=True, causal=Tru
             h = hq // G
             K, V, inv = c.stored(b, h)
             if c.ctx[b]:
-                _, sk, _ = co.oracle_quantise(np64(c.k[b, h, :c.ctx[b]]), c.group)
-                _, _, zv = co.oracle_quantise(np64(c.v[b, h, :c.ctx[b]]), c.group)
-                zV = np.repeat(zv, c.group, axis=1)
+                _, _, zk = co.oracle_quantise(np64(c.k[b, h, :c.ctx[b]]), c.group)
+                _, sv, zv = co.oracle_quantise(np64(c.v[b, h, :c.ctx[b]]), c.group)
+                zK, zV, sV = (np.repeat(x, c.group, axis=1) for x in (zk, zv, sv))
             for t in range(T):
                 pos = c.ctx[b] - new[b] + t
                 got, gl = np64(out[b, hq, t]), float(lse[b, hq, t])
@@ -256,8 +254,9 @@ def _check_attend(c, q, out, lse, new, selected=None, self_mask=True, causal=Tru
                 if keys.size == 0:
                     assert (got == 0).all() and gl == -np.inf, (b, hq, t)
                     continue
-                ks = (sk[keys].max(1) * (inv[keys] if unit_keys else 1.0)).max()
-                bound, lb = _bounds(np64(q[b, hq, t]), V[keys], zV[keys], ks, w, D, c.group, sc, f32_in, f32_out, want)
+                ks = sc * (inv[keys] if unit_keys else np.ones(keys.size))
+                bound, lb = _bounds(np64(q[b, hq, t]), K[keys], zK[keys], V[keys], zV[keys], sV[keys], w, ks, f32_in,
+                                    f32_out, want)
                 assert (np.abs(got - want) <= bound).all(), (b, hq, t, np.abs(got - want).max(), bound.min())
                 assert abs(gl - wl) <= lb + 2.0 ** -22 * abs(wl), (b, hq, t, gl, wl)
 
