@@ -10,6 +10,7 @@ happens in the library's CUDA kernels; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -304,20 +305,34 @@ def lsh_chunk_attend_backward(qk, v, perm, chunk, out, lse, dout, *, self_mask=T
     return dqk, dv
 
 
-def _on_device(dev, stream, tensors, call, where):
-    """Runs ``call(stream pointer)`` with ``dev`` current; every tensor must be on ``dev``."""
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{where}: all tensors must be on {dev}")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"{where}: the stream must be on {dev}")
-    if torch.cuda.current_device() == dev.index:
-        _check(call(_stream(stream)), where)
+def _fit(t, name, dtype, shape, dev):
+    """``_need`` and the device, with one cheap test where all is well; returns the data pointer."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous() and t.is_cuda):
+        return t.data_ptr()
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _on_device(dev, stream, fn, where, *args):
+    """Calls ``fn(*args, stream pointer)`` with ``dev`` current (decoding steps are short: no more host work
+    than it takes)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    else:
+        if stream.device != dev:
+            raise ValueError(f"{where}: the stream must be on {dev}")
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev.index:
+        code = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            _check(call(_stream(stream)), where)
+            code = fn(*args, raw)
+    if code:
+        raise LSHError(code, where)
 
 
+@functools.lru_cache(maxsize=256)
 def lsh_cache_block_bytes(page, D, group):
     """Bytes of one (page, head) block of the 4-bit cache (0 for a form that no kernel serves)."""
     return int(load_library().lsh_cache_block_bytes(page, D, group))
@@ -338,25 +353,43 @@ def alloc_cache(n_pages, H, D, *, page=64, group=64, n_rounds=0, device="cuda"):
     return cache, tags
 
 
-def _need_cache(cache, H, D, page, group):
-    _need(cache, "cache", torch.uint8)
+def _need_cache(cache, D, page, group):
+    """(n_pages, H) of a cache of that form; its device is the call's."""
     block = lsh_cache_block_bytes(page, D, group)
     if block == 0:
         raise LSHError(8, f"no cache of page {page}, head dim {D}, group {group}")
-    if cache.dim() != 3 or cache.shape[1] != H or cache.shape[2] != block:
-        raise ValueError(f"cache must be [n_pages, {H}, {block}], got {tuple(cache.shape)}")
-    return cache.shape[0]
+    _need(cache, "cache", torch.uint8)
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] != block:
+        raise ValueError(f"cache must be [n_pages, H, {block}], got {tuple(shape)}")
+    return shape[0], shape[1]
 
 
-def _need_lengths(page_table, ctx_len, new_len):
+def _need_pages(page_table, ctx_len, new_len, dev):
+    """(B, max_pages, the three pointers)."""
     _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2:
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
-    _need(ctx_len, "ctx_len", torch.int32, (B,))
-    if new_len is not None:
-        _need(new_len, "new_len", torch.int32, (B,))
-    return B, max_pages
+    lengths = (shape[0],)
+    return (shape[0], shape[1], _fit(page_table, "page_table", torch.int32, shape, dev),
+            _fit(ctx_len, "ctx_len", torch.int32, lengths, dev),
+            None if new_len is None else _fit(new_len, "new_len", torch.int32, lengths, dev))
+
+
+def _new(t, name, dtype, shape, dev):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _fit(t, name, dtype, shape, dev)
+
+
+def _rows4(t, name):
+    _need(t, name)
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions")
+    return t.shape
 
 
 def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_len=None, buckets=None, tags=None,
@@ -368,29 +401,25 @@ def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_
     ``buckets`` [B,H,n_rounds,T] (``lsh_hash``) and ``tags`` the rows' buckets are kept as well.
     """
     lib = load_library()
-    _need(k, "k")
-    if k.dim() != 4:
-        raise ValueError("k must be [B, H, T, D]")
-    B, H, T, D = k.shape
-    _need(v, "v", k.dtype, k.shape)
-    n_pages = _need_cache(cache, H, D, page, group)
-    Bt, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    B, H, T, D = shape = _rows4(k, "k")
+    dt = _dt(k)
+    dev = k.device
+    n_pages, Hc = _need_cache(cache, D, page, group)
+    if Hc != H:
+        raise ValueError(f"cache has {Hc} heads, k {H}")
+    Bt, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
     if Bt != B:
         raise ValueError(f"page_table has {Bt} sequences, k {B}")
-    n_rounds = 0
+    n_rounds, bk, tg = 0, None, None
     if buckets is not None or tags is not None:
         if buckets is None or tags is None:
             raise ValueError("buckets and tags go together")
-        _need(tags, "tags", torch.int16)
-        if tags.dim() != 4:
-            raise ValueError("tags must be [n_pages, H, n_rounds, page]")
-        n_rounds = tags.shape[2]
-        _need(tags, "tags", torch.int16, (n_pages, H, n_rounds, page))
-        _need(buckets, "buckets", torch.int32, (B, H, n_rounds, T))
-    _on_device(k.device, stream, (v, cache, page_table, ctx_len, new_len, buckets, tags),
-               lambda s: lib.lsh_cache_write(_ptr(k), _ptr(v), _dt(k), B, H, T, D, _ptr(buckets), n_rounds,
-                                             _ptr(ctx_len), _ptr(new_len), _ptr(page_table), max_pages, page, group,
-                                             _ptr(cache), n_pages, _ptr(tags), s), "lsh_cache_write")
+        n_rounds = _rows4(tags, "tags")[2]
+        tg = _fit(tags, "tags", torch.int16, (n_pages, H, n_rounds, page), dev)
+        bk = _fit(buckets, "buckets", torch.int32, (B, H, n_rounds, T), dev)
+    _on_device(dev, stream, lib.lsh_cache_write, "lsh_cache_write", k.data_ptr(), _fit(v, "v", k.dtype, shape, dev), dt,
+               B, H, T, D, bk, n_rounds, ctx, new, table, max_pages, page, group,
+               _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, tg)
 
 
 def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_len=None, out_dtype=torch.bfloat16,
@@ -401,24 +430,17 @@ def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_l
     they were written); padding rows are 0.  ``new_len=ctx_len`` reads whole sequences.
     """
     lib = load_library()
-    _need(cache, "cache", torch.uint8)
-    if cache.dim() != 3:
-        raise ValueError("cache must be [n_pages, H, block]")
-    H = cache.shape[1]
-    n_pages = _need_cache(cache, H, D, page, group)
-    B, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    n_pages, H = _need_cache(cache, D, page, group)
+    dev = cache.device
+    B, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
     if out_dtype not in _DT:
         raise ValueError(f"unsupported dtype {out_dtype}")
-    dev = cache.device
-    k = torch.empty((B, H, T, D), dtype=out_dtype, device=dev) if k is None else _need(k, "k", out_dtype, (B, H, T, D))
-    v = torch.empty((B, H, T, D), dtype=out_dtype, device=dev) if v is None else _need(v, "v", out_dtype, (B, H, T, D))
-    if key_inv is None:
-        key_inv = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-    _need(key_inv, "key_inv", torch.float32, (B, H, T))
-    _on_device(dev, stream, (page_table, ctx_len, new_len, k, v, key_inv),
-               lambda s: lib.lsh_cache_read(_ptr(cache), n_pages, B, H, T, D, _ptr(ctx_len), _ptr(new_len),
-                                            _ptr(page_table), max_pages, page, group, _ptr(k), _ptr(v),
-                                            _DT[out_dtype], _ptr(key_inv), s), "lsh_cache_read")
+    shape = (B, H, T, D)
+    k, kp = _new(k, "k", out_dtype, shape, dev)
+    v, vp = _new(v, "v", out_dtype, shape, dev)
+    key_inv, ip = _new(key_inv, "key_inv", torch.float32, shape[:3], dev)
+    _on_device(dev, stream, lib.lsh_cache_read, "lsh_cache_read", cache.data_ptr(), n_pages, B, H, T, D, ctx, new, table,
+               max_pages, page, group, kp, vp, _DT[out_dtype], ip)
     return k, v, key_inv
 
 
@@ -432,32 +454,31 @@ def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=
     ascending, padded with -1.
     """
     lib = load_library()
-    _need(tags, "tags", torch.int16)
-    if tags.dim() != 4:
-        raise ValueError("tags must be [n_pages, H, n_rounds, page]")
-    n_pages, H, n_rounds, page = tags.shape
-    B, max_pages = _need_lengths(page_table, ctx_len, new_len)
-    _need(q_buckets, "q_buckets", torch.int32)
-    if q_buckets.dim() != 4 or q_buckets.shape[0] != B or q_buckets.shape[2] != n_rounds:
-        raise ValueError(f"q_buckets must be [{B}, Hq, {n_rounds}, T]")
-    Hq, T = q_buckets.shape[1], q_buckets.shape[3]
+    n_pages, H, n_rounds, page = _rows4(tags, "tags")
     dev = tags.device
-    if selected is None:
-        selected = torch.empty((B, H, T, n_select), dtype=torch.int32, device=dev)
-    if scores is None:
-        scores = torch.empty((B, H, T, max_pages), dtype=torch.int32, device=dev)
-    _need(selected, "selected", torch.int32, (B, H, T, n_select))
-    _need(scores, "scores", torch.int32, (B, H, T, max_pages))
-    _on_device(dev, stream, (q_buckets, page_table, ctx_len, new_len, selected, scores),
-               lambda s: lib.lsh_cache_select(_ptr(tags), n_pages, _ptr(q_buckets), B, Hq, H, T, n_rounds,
-                                              _ptr(ctx_len), _ptr(new_len), _ptr(page_table), max_pages, page,
-                                              n_select, n_local, 2 if causal else 0, _ptr(selected), _ptr(scores),
-                                              s), "lsh_cache_select")
+    B, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
+    Bq, Hq, Rq, T = _rows4(q_buckets, "q_buckets")
+    if Bq != B or Rq != n_rounds:
+        raise ValueError(f"q_buckets must be [{B}, Hq, {n_rounds}, T]")
+    if n_select < 1:
+        raise ValueError("n_select must be at least 1")
+    selected, sp = _new(selected, "selected", torch.int32, (B, H, T, n_select), dev)
+    scores, cp = _new(scores, "scores", torch.int32, (B, H, T, max_pages), dev)
+    _on_device(dev, stream, lib.lsh_cache_select, "lsh_cache_select",
+               _fit(tags, "tags", torch.int16, tags.shape, dev), n_pages,
+               _fit(q_buckets, "q_buckets", torch.int32, q_buckets.shape, dev), B, Hq, H, T, n_rounds, ctx, new, table,
+               max_pages, page, n_select, n_local, 2 if causal else 0, sp, cp)
     return selected, scores
 
 
+@functools.lru_cache(maxsize=1024)
+def _attend_workspace(dt, B, Hq, H, T, D, max_pages, page, n_select, dev_index):
+    with torch.cuda.device(dev_index):
+        return int(load_library().lsh_cache_attend_workspace_bytes(dt, B, Hq, H, T, D, max_pages, page, n_select))
+
+
 def lsh_cache_attend_workspace_bytes(dtype, B, Hq, H, T, D, max_pages, page, n_select=0):
-    """Bytes of scratch that ``lsh_cache_attend`` needs for these sizes."""
+    """Bytes of scratch that ``lsh_cache_attend`` needs for these sizes on the current device."""
     return int(load_library().lsh_cache_attend_workspace_bytes(_DT[dtype], B, Hq, H, T, D, max_pages, page, n_select))
 
 
@@ -472,48 +493,31 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
     ``unit_keys``: keys are length-normalised.  Rows without a key (padding) get 0 and -inf.
     """
     lib = load_library()
-    _need(q, "q")
-    _need(cache, "cache", torch.uint8)
-    if q.dim() != 4 or cache.dim() != 3:
-        raise ValueError("q must be [B, Hq, T, D] and cache [n_pages, H, block]")
-    B, Hq, T, D = q.shape
-    H = cache.shape[1]
-    n_pages = _need_cache(cache, H, D, page, group)
-    Bt, max_pages = _need_lengths(page_table, ctx_len, new_len)
+    B, Hq, T, D = shape = _rows4(q, "q")
+    dt = _dt(q)
+    dev = q.device
+    n_pages, H = _need_cache(cache, D, page, group)
+    Bt, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
     if Bt != B:
         raise ValueError(f"page_table has {Bt} sequences, q {B}")
-    n_select = 0
+    n_select, sel = 0, None
     if selected is not None:
-        _need(selected, "selected", torch.int32)
-        if selected.dim() != 4:
-            raise ValueError("selected must be [B, H, T, n_select]")
-        n_select = selected.shape[3]
-        _need(selected, "selected", torch.int32, (B, H, T, n_select))
+        n_select = _rows4(selected, "selected")[3]
+        sel = _fit(selected, "selected", torch.int32, (B, H, T, n_select), dev)
     out_dtype = q.dtype if out_dtype is None else out_dtype
     if out_dtype not in _DT:
         raise ValueError(f"unsupported dtype {out_dtype}")
-    dev = q.device
-    if out is None:
-        out = torch.empty((B, Hq, T, D), dtype=out_dtype, device=dev)
-    if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-    _need(out, "out", out_dtype, (B, Hq, T, D))
-    _need(lse, "lse", torch.float32, (B, Hq, T))
-    dt = _dt(q)
+    out, op = _new(out, "out", out_dtype, shape, dev)
+    lse, lp = _new(lse, "lse", torch.float32, shape[:3], dev)
     if workspace is None:
-        need = int(lib.lsh_cache_attend_workspace_bytes(dt, B, Hq, H, T, D, max_pages, page, n_select))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    else:
-        _need(workspace, "workspace", torch.uint8)
-    sc = 0.0 if scale is None else float(scale)
-    mask = (1 if self_mask else 0) | (2 if causal else 0)
-    _on_device(dev, stream, (cache, page_table, ctx_len, new_len, selected, out, lse, workspace),
-               lambda s: lib.lsh_cache_attend(_ptr(q), dt, B, Hq, H, T, D, _ptr(cache), n_pages, _ptr(ctx_len),
-                                              _ptr(new_len), _ptr(page_table), max_pages, page, group,
-                                              _ptr(selected), n_select, mask, 1 if unit_keys else 0, sc, _ptr(out),
-                                              _DT[out_dtype], _ptr(lse), _ptr(workspace),
-                                              workspace.numel() if workspace is not None else 0, s),
-               "lsh_cache_attend")
+        need = _attend_workspace(dt, B, Hq, H, T, D, max_pages, page, n_select, dev.index)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    nbytes = workspace.numel()
+    ws = _fit(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _on_device(dev, stream, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D,
+               _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, ctx, new, table, max_pages, page, group, sel,
+               n_select, (1 if self_mask else 0) | (2 if causal else 0), 1 if unit_keys else 0,
+               0.0 if scale is None else float(scale), op, _DT[out_dtype], lp, ws, nbytes)
     return out, lse
 
 
@@ -568,6 +572,11 @@ def lsh_attention_decode(qk, v, R, n_buckets, cache, tags, page_table, ctx_len, 
     b = bufs or {}
     if n_select and tags is None:
         raise ValueError("n_select needs tags")
+    if isinstance(qk, torch.Tensor) and qk.is_cuda and torch.cuda.current_device() != qk.device.index:
+        with torch.cuda.device(qk.device):
+            return lsh_attention_decode(qk, v, R, n_buckets, cache, tags, page_table, ctx_len, page=page, group=group,
+                                        new_len=new_len, n_select=n_select, n_local=n_local, self_mask=self_mask,
+                                        scale=scale, stream=stream, bufs=bufs, check=check)
     buckets = None
     if tags is not None:
         buckets, _ = lsh_hash(qk, R, n_buckets, buckets=b.get("buckets"), with_near_tie=False, stream=stream)

@@ -88,13 +88,25 @@ inline size_t attend_plan_bytes(const AttendPlan& p, int D) {
   return n * D * sizeof(float) + n * 2 * sizeof(float);
 }
 
+// Sets a kernel's dynamic shared memory limit once per device (the call costs as much as a launch).
+inline lsh_status allow_smem(const void* fn, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return LSH_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return LSH_OK;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return LSH_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return LSH_OK;
+}
+
 template <typename TQ, int D, int GROUP, int CW, int NT>
 lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   using namespace lsh::cache;
   using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   auto kfn = cache_attend_kernel<TQ, D, GROUP, CW, NT>;
-  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-    return LSH_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  const lsh_status st = allow_smem((const void*)kfn, C::kSmem, done);
+  if (st != LSH_OK) return st;
   static_assert(C::kCtas >= 1 && C::kCtas <= kMaxCtasPerSm, "workspace is sized for it");
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
   a.nc = std::min(p.max_ctas, sms * C::kCtas);
