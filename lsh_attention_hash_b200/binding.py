@@ -377,12 +377,15 @@ def _need_pages(page_table, ctx_len, new_len, dev):
             None if new_len is None else _fit(new_len, "new_len", torch.int32, lengths, dev))
 
 
-def _new(t, name, dtype, shape, dev):
-    """(tensor, pointer) of an output: the caller's, checked, or a new one."""
+def _new(t, name, dtype, shape, like):
+    """(tensor, pointer) of an output: the caller's, checked, or a new one on ``like``'s device."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        if dtype is like.dtype and shape == like.shape:
+            t = torch.empty_like(like)  # (the quickest of torch's calls)
+        else:
+            t = like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
-    return t, _fit(t, name, dtype, shape, dev)
+    return t, _fit(t, name, dtype, shape, like.device)
 
 
 def _rows4(t, name):
@@ -436,9 +439,9 @@ def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_l
     if out_dtype not in _DT:
         raise ValueError(f"unsupported dtype {out_dtype}")
     shape = (B, H, T, D)
-    k, kp = _new(k, "k", out_dtype, shape, dev)
-    v, vp = _new(v, "v", out_dtype, shape, dev)
-    key_inv, ip = _new(key_inv, "key_inv", torch.float32, shape[:3], dev)
+    k, kp = _new(k, "k", out_dtype, shape, cache)
+    v, vp = _new(v, "v", out_dtype, shape, k)
+    key_inv, ip = _new(key_inv, "key_inv", torch.float32, shape[:3], cache)
     _on_device(dev, stream, lib.lsh_cache_read, "lsh_cache_read", cache.data_ptr(), n_pages, B, H, T, D, ctx, new, table,
                max_pages, page, group, kp, vp, _DT[out_dtype], ip)
     return k, v, key_inv
@@ -462,8 +465,8 @@ def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=
         raise ValueError(f"q_buckets must be [{B}, Hq, {n_rounds}, T]")
     if n_select < 1:
         raise ValueError("n_select must be at least 1")
-    selected, sp = _new(selected, "selected", torch.int32, (B, H, T, n_select), dev)
-    scores, cp = _new(scores, "scores", torch.int32, (B, H, T, max_pages), dev)
+    selected, sp = _new(selected, "selected", torch.int32, (B, H, T, n_select), tags)
+    scores, cp = _new(scores, "scores", torch.int32, (B, H, T, max_pages), tags)
     _on_device(dev, stream, lib.lsh_cache_select, "lsh_cache_select",
                _fit(tags, "tags", torch.int16, tags.shape, dev), n_pages,
                _fit(q_buckets, "q_buckets", torch.int32, q_buckets.shape, dev), B, Hq, H, T, n_rounds, ctx, new, table,
@@ -507,11 +510,11 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
     out_dtype = q.dtype if out_dtype is None else out_dtype
     if out_dtype not in _DT:
         raise ValueError(f"unsupported dtype {out_dtype}")
-    out, op = _new(out, "out", out_dtype, shape, dev)
-    lse, lp = _new(lse, "lse", torch.float32, shape[:3], dev)
+    out, op = _new(out, "out", out_dtype, shape, q)
+    lse, lp = _new(lse, "lse", torch.float32, shape[:3], q)
     if workspace is None:
         need = _attend_workspace(dt, B, Hq, H, T, D, max_pages, page, n_select, dev.index)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
     nbytes = workspace.numel()
     ws = _fit(workspace, "workspace", torch.uint8, workspace.shape, dev)
     _on_device(dev, stream, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D,

@@ -237,9 +237,19 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
   a.causal = (mask & LSH_MASK_CAUSAL) ? 1 : 0;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   cudaStream_t s = as_stream(stream);
-  const long long warps = (long long)B * H * max_pages;
+  const int groups = (max_pages + lsh::cache::kWarpPages - 1) / lsh::cache::kWarpPages;
   const int per = lsh::cache::kScoreThreads / 32;
-  if (warps > 0) lsh::cache::cache_score_kernel<<<(unsigned)((warps + per - 1) / per), lsh::cache::kScoreThreads, 0, s>>>(a);
+  const long long ctas = ((long long)B * H * groups + per - 1) / per;
+  if (ctas > 0) {
+    const unsigned grid = (unsigned)ctas;
+    const int threads = lsh::cache::kScoreThreads;
+    // a lane's chunks of a page in registers for one query head and up to 8 rounds of 128 tokens
+    const int chunks = a.G == 1 && n_rounds * page % 256 == 0 ? n_rounds * page / 256 : 0;
+    if (chunks == 1) lsh::cache::cache_score_kernel<1><<<grid, threads, 0, s>>>(a, groups);
+    else if (chunks == 2) lsh::cache::cache_score_kernel<2><<<grid, threads, 0, s>>>(a, groups);
+    else if (chunks == 4) lsh::cache::cache_score_kernel<4><<<grid, threads, 0, s>>>(a, groups);
+    else lsh::cache::cache_score_kernel<0><<<grid, threads, 0, s>>>(a, groups);
+  }
   const int smem = max_pages > n_select ? max_pages * 4 : 16;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(lsh::cache::cache_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=

@@ -261,6 +261,9 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   int slot = 0;
   uint32_t phase = 0;
 
+  // the join may be set up (it waits for this kernel's end before it reads): every CTA is resident
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // ---- the CTA's stretch of the work -----------------------------------------------------------------
   long long total, before;
   work_before(a, 0, lane, total, before);
@@ -289,8 +292,76 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   tc::fence_proxy_async_smem();  // (the last item's sums lay where copies go now)
   __syncthreads();
 
-  // ---- set-up of the item: query operands and sums -----------------------------------------------------
   const int32_t* picks = sel ? a.selected + (((long long)b * a.pg.H + h) * a.pg.T + row_t) * a.n_select : nullptr;
+  // ---- pages and copies: first of all, so that the first copies run under the rest of the set-up --------
+  int tile0 = tile_lo, tile1 = tile_lo, e0 = 0;  // the tiles whose pages are looked up, in list order
+  auto look_up = [&]() {  // the next ones, as many pages as are held at a time (table and, with selection, list)
+    tile0 = tile1;
+    e0 = (tile0 << 4) >> pl;
+    tile1 = (int)min((long long)tile_hi, ((long long)(e0 + kMaxEntries) << pl) >> 4);
+    const int n_ent = (((tile1 - 1) << 4) >> pl) - e0 + 1;
+    for (int i = tid; i < n_ent; i += kAttThreads) {
+      int logical = e0 + i;
+      if (sel) logical = picks[e0 + i];
+      int phys = -1;
+      if (logical >= 0 && logical < a.pg.max_pages && ((long long)logical << pl) < u.ctx) phys = page_of(a.pg, b, logical);
+      Entry e;
+      e.src = phys >= 0 ? a.cache + tile_offset(a.pg, phys, h, 0, F::kTile) : nullptr;
+      e.pos = logical << pl;
+      e.pad = 0;
+      ent[i] = e;
+    }
+  };
+  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st
+    const int tile = tile0 + st * ST;
+    const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
+    if (pl >= 6) {  // a stage lies inside a page
+      const Entry e = ent[((tile << 4) >> pl) - e0];
+      const int in_page = tile & ((1 << (pl - 4)) - 1);
+      const int p = e.pos + (in_page << 4);
+      // tiles that hold tokens of the sequence (in list order the sequence may end before the list)
+      const int n = e.src ? min(min(ST, tile1 - tile), max(0, (u.ctx - p + kTileTokens - 1) >> 4)) : 0;
+      desc[slot] = make_int4(n > 0 ? p : -1, n > 1 ? p + 16 : -1, n > 2 ? p + 32 : -1, n > 3 ? p + 48 : -1);
+      tc::mbar_arrive_expect_tx(bar + slot, n * F::kTile);
+      if (n > 0) bulk_load(dst, e.src + in_page * F::kTile, n * F::kTile, bar + slot);
+      return;
+    }
+    const uint8_t* src[ST];
+    int first[ST];
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+      src[k] = nullptr;
+      first[k] = -1;
+      if (tile + k < tile1) {
+        const Entry e = ent[(((tile + k) << 4) >> pl) - e0];
+        const int in_page = (tile + k) & ((1 << (pl - 4)) - 1);
+        const int p = e.pos + (in_page << 4);
+        if (e.src && p < u.ctx) {
+          src[k] = e.src + in_page * F::kTile;
+          first[k] = p;
+          bytes += F::kTile;
+        }
+      }
+    }
+    desc[slot] = make_int4(first[0], first[1], first[2], first[3]);
+    tc::mbar_arrive_expect_tx(bar + slot, bytes);
+#pragma unroll
+    for (int k = 0; k < ST; ++k)
+      if (src[k]) bulk_load(dst + k * F::kTile, src[k], F::kTile, bar + slot);
+  };
+  auto start = [&]() {  // the warp's first copies
+    const int n_stage = (tile1 - tile0 + ST - 1) / ST;
+    if (lane == 0)
+      for (int i = 0, s2 = slot; i < kStages; ++i) {
+        if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, s2);
+        s2 = s2 + 1 == kStages ? 0 : s2 + 1;
+      }
+    __syncwarp();
+  };
+
+  // ---- set-up of the item: query operands and sums -----------------------------------------------------
+  look_up();
   auto q_row = [&](int col) -> const TQ* {
     const int tt = sel ? row_t : col / a.G, gg = sel ? col : col - tt * a.G;
     return static_cast<const TQ*>(a.q) + (((long long)b * a.pg.H + h) * a.G + gg) * (long long)a.pg.T * D +
@@ -320,6 +391,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     if (j == 0) qstep[cc] = top / C::kTop;
   }
   __syncthreads();
+  start();
   // B operands of K's products: columns 2 k, 2 k + 1 of a fragment are the upper and lower byte (the third
   // byte and nothing, in the second set) of slot k = i CW + c, that is of query column c for tile i, and
   // zero for the other tiles; word w covers dims 32 w .. 32 w + 31.  Bytes are signed, so a lower
@@ -412,46 +484,6 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     for (int n = 0; n < NG; ++n) zs[nt][n] = 0.f;
   }
 
-  // ---- the warp's pipeline ------------------------------------------------------------------------
-  int tile0 = tile_lo, tile1 = tile_lo, e0 = 0;  // the tiles whose pages are looked up, in list order
-  auto issue = [&](int st, int slot) {  // lane 0: copies of stage st
-    const int tile = tile0 + st * ST;
-    const uint32_t dst = tc::smem_u32(ring + slot * C::kStageBytes);
-    if (pl >= 6) {  // a stage lies inside a page
-      const Entry e = ent[((tile << 4) >> pl) - e0];
-      const int in_page = tile & ((1 << (pl - 4)) - 1);
-      const int p = e.pos + (in_page << 4);
-      // tiles that hold tokens of the sequence (in list order the sequence may end before the list)
-      const int n = e.src ? min(min(ST, tile1 - tile), max(0, (u.ctx - p + kTileTokens - 1) >> 4)) : 0;
-      desc[slot] = make_int4(n > 0 ? p : -1, n > 1 ? p + 16 : -1, n > 2 ? p + 32 : -1, n > 3 ? p + 48 : -1);
-      tc::mbar_arrive_expect_tx(bar + slot, n * F::kTile);
-      if (n > 0) bulk_load(dst, e.src + in_page * F::kTile, n * F::kTile, bar + slot);
-      return;
-    }
-    const uint8_t* src[ST];
-    int first[ST];
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int k = 0; k < ST; ++k) {
-      src[k] = nullptr;
-      first[k] = -1;
-      if (tile + k < tile1) {
-        const Entry e = ent[(((tile + k) << 4) >> pl) - e0];
-        const int in_page = (tile + k) & ((1 << (pl - 4)) - 1);
-        const int p = e.pos + (in_page << 4);
-        if (e.src && p < u.ctx) {
-          src[k] = e.src + in_page * F::kTile;
-          first[k] = p;
-          bytes += F::kTile;
-        }
-      }
-    }
-    desc[slot] = make_int4(first[0], first[1], first[2], first[3]);
-    tc::mbar_arrive_expect_tx(bar + slot, bytes);
-#pragma unroll
-    for (int k = 0; k < ST; ++k)
-      if (src[k]) bulk_load(dst + k * F::kTile, src[k], F::kTile, bar + slot);
-  };
   // One stage of ST tiles.  MASKED: a tile may be missing, and every key is tested against the columns.
   auto consume = [&](const uint8_t* buf, const int* first, auto masked_c) {  // first: positions, in shared memory
     constexpr bool MASKED = decltype(masked_c)::value;
@@ -671,32 +703,8 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     }
   };
 
-  while (tile1 < tile_hi) {
-  // pages of the next tiles (the table and, with selection, the list), as many as are held at a time
-  tile0 = tile1;
-  e0 = (tile0 << 4) >> pl;
-  tile1 = (int)min((long long)tile_hi, ((long long)(e0 + kMaxEntries) << pl) >> 4);
-  const int n_ent = (((tile1 - 1) << 4) >> pl) - e0 + 1;
-  if (tile0 != tile_lo) __syncthreads();
-  for (int i = tid; i < n_ent; i += kAttThreads) {
-    int logical = e0 + i;
-    if (sel) logical = picks[e0 + i];
-    int phys = -1;
-    if (logical >= 0 && logical < a.pg.max_pages && ((long long)logical << pl) < u.ctx) phys = page_of(a.pg, b, logical);
-    Entry e;
-    e.src = phys >= 0 ? a.cache + tile_offset(a.pg, phys, h, 0, F::kTile) : nullptr;
-    e.pos = logical << pl;
-    e.pad = 0;
-    ent[i] = e;
-  }
-  __syncthreads();
+  for (;;) {
   const int n_stage = (tile1 - tile0 + ST - 1) / ST;
-  if (lane == 0)
-    for (int i = 0, s2 = slot; i < kStages; ++i) {
-      if (warp + i * kAttWarps < n_stage) issue(warp + i * kAttWarps, s2);
-      s2 = s2 + 1 == kStages ? 0 : s2 + 1;
-    }
-  __syncwarp();
   for (int st = warp; st < n_stage; st += kAttWarps) {
     if (!tc::mbar_wait(bar + slot, phase, &abort_flag)) {
       // give the copies in flight the same time each, then leave
@@ -725,6 +733,11 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       phase ^= 1;
     }
   }
+  if (tile1 >= tile_hi) break;
+  __syncthreads();
+  look_up();
+  __syncthreads();
+  start();
   }
 
   // ---- join the warps -----------------------------------------------------------------------------

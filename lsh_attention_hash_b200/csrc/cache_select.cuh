@@ -6,11 +6,12 @@
 // over the page's admissible positions of [tag == bucket of the query].  Whole
 // numbers, so the choice is the same however the sum is split.
 //
-// Scoring reads 2 bytes per token and round and is bound by that: one warp per
-// (page, head), 16-byte loads, two tags per comparison.  The choice is one CTA per
-// query row over its scores in shared memory: a binary search for the lowest score
-// that gets in, then one pass that writes the chosen pages in ascending order, of
-// equal scores those of the lowest pages.
+// Scoring reads 2 bytes per token and round and is bound by that: a warp takes eight
+// pages of a head, all 16-byte loads of a page (and of the next ones) in flight, and compares two
+// tags an instruction: min(tag ^ bucket, 1) counts those that differ.  The choice is one CTA per
+// query row over its scores in shared memory: a binary search for the lowest score that gets
+// in, then one pass that writes the chosen pages in ascending order, of equal scores those of the
+// lowest pages.
 #pragma once
 
 #include "cache_common.cuh"
@@ -19,6 +20,7 @@ namespace lsh {
 namespace cache {
 
 constexpr int kScoreThreads = 256;
+constexpr int kWarpPages = 8;  // pages of a warp
 constexpr int kPickThreads = 512;
 constexpr int kMaxPickPages = 49152;  // scores of one row in shared memory (192 KB)
 
@@ -38,53 +40,100 @@ __device__ __forceinline__ int select_limit(const SelectArgs& a, int b, int t) {
   return a.causal ? pos + 1 : ctx_of(a.pg, b);
 }
 
-__global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectArgs a) {
-  const long long w = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+// How many of the tags in a word's two halves differ from q's (a count in each half).
+__device__ __forceinline__ uint32_t differ2(uint32_t tags, uint32_t q2) {
+  return __vminu2(tags ^ q2, 0x00010001u);
+}
+
+// NC: 16-byte chunks of a page per lane (n_rounds * page / 256) when the page is whole and there is one
+// query head, so that the lane's buckets stay in registers; 0: any number.
+template <int NC>
+__global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectArgs a, int groups) {
   const int lane = threadIdx.x & 31;
   const Pages& pg = a.pg;
-  const long long bh = w / pg.max_pages;
-  if (bh >= (long long)a.B * pg.H) return;
-  const int lp = (int)(w - bh * pg.max_pages);
-  const int b = (int)(bh / pg.H), h = (int)(bh - (long long)b * pg.H);
-  const int page = 1 << pg.page_log2, first = lp << pg.page_log2;
-  const int chunks_log2 = pg.page_log2 - 3;  // 16-byte chunks of a round
-  const int n_chunks = a.n_rounds << chunks_log2;
-  int phys = -2;
+  const unsigned w = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);  // (head, 8 pages)
+  const unsigned bh = w / groups;
+  if (bh >= (unsigned)(a.B * pg.H)) return;
+  const int lp0 = (int)(w - bh * groups) * kWarpPages;
+  const int b = bh / pg.H, h = bh - b * pg.H;
+  const int page = 1 << pg.page_log2;
+  const int cl = pg.page_log2 - 3;  // log2 of the 16-byte chunks of a round
+  const int n_chunks = a.n_rounds << cl;
+  const int mine = lp0 + lane;      // lanes 0..7 have a page each
+  const bool has = lane < kWarpPages && mine < pg.max_pages;
+  int phys = -2;                    // of the lane's page, once it is wanted
+  const long long row_bytes = (long long)a.n_rounds * page * 2;
   for (int t = 0; t < pg.T; ++t) {
     const int limit = select_limit(a, b, t);
-    int score = -1;
-    if (first < limit) {
-      if (phys == -2) phys = page_of(pg, b, lp);
+    if (has && phys == -2 && (mine << pg.page_log2) < limit) phys = page_of(pg, b, mine);
+    const int32_t* qb = a.q_buckets + ((long long)bh * a.G * a.n_rounds) * pg.T + t;
+    int score = has && (mine << pg.page_log2) < limit ? 0 : -1;
+    const int whole = min(kWarpPages, max(0, (limit >> pg.page_log2) - lp0));  // pages below the limit
+    int i = 0;
+    if (NC > 0) {
+      uint32_t q2[NC > 0 ? NC : 1];
+      bool bad = false;  // a bucket that no tag holds: then the general loop
+#pragma unroll
+      for (int k = 0; k < NC; ++k) {
+        const uint32_t q = (uint32_t)qb[(long long)((lane + 32 * k) >> cl) * pg.T];
+        bad |= q > 65535u;
+        q2[k] = q * 0x10001u;
+      }
+      if (!__any_sync(0xffffffffu, bad)) {
+#pragma unroll 4
+        for (; i < whole; ++i) {
+          const int ph = __shfl_sync(0xffffffffu, phys, i);
+          uint32_t acc = 0;
+          if (ph >= 0) {
+            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.tags) +
+                                                              ((long long)ph * pg.H + h) * row_bytes) + lane;
+            uint4 u[NC > 0 ? NC : 1];
+#pragma unroll
+            for (int k = 0; k < NC; ++k) u[k] = __ldg(src + 32 * k);
+            acc = NC * 0x00040004u;
+#pragma unroll
+            for (int k = 0; k < NC; ++k)
+              acc -= differ2(u[k].x, q2[k]) + differ2(u[k].y, q2[k]) + differ2(u[k].z, q2[k]) + differ2(u[k].w, q2[k]);
+          }
+          const int sum = __reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
+          if (lane == i) score = sum;
+        }
+      }
+    }
+    // the page that the limit cuts, other sizes, several query heads
+    for (; i < kWarpPages && ((lp0 + i) << pg.page_log2) < limit; ++i) {
+      const int ph = __shfl_sync(0xffffffffu, phys, i);
+      const int first = (lp0 + i) << pg.page_log2;
       uint32_t acc = 0;
-      if (phys >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            a.tags + (((long long)phys * pg.H + h) * a.n_rounds) * page);
+      if (ph >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.tags) +
+                                                          ((long long)ph * pg.H + h) * row_bytes);
         for (int c = lane; c < n_chunks; c += 32) {
           const uint4 u = __ldg(src + c);
-          const int n = c >> chunks_log2;
-          const int ok = limit - first - ((c & ((1 << chunks_log2) - 1)) << 3);  // admissible tokens of the chunk
+          const int n = c >> cl;
+          const int ok = limit - first - ((c & ((1 << cl) - 1)) << 3);  // admissible tokens of the chunk
           const uint32_t m0 = ok >= 2 ? 0x10001u : (ok == 1 ? 1u : 0u);
           const uint32_t m1 = ok >= 4 ? 0x10001u : (ok == 3 ? 1u : 0u);
           const uint32_t m2 = ok >= 6 ? 0x10001u : (ok == 5 ? 1u : 0u);
           const uint32_t m3 = ok >= 8 ? 0x10001u : (ok == 7 ? 1u : 0u);
-          const int32_t* qb = a.q_buckets + (((long long)b * pg.H + h) * a.G * a.n_rounds + n) * pg.T + t;
           for (int g = 0; g < a.G; ++g) {
-            const uint32_t q = (uint32_t)__ldg(qb + (long long)g * a.n_rounds * pg.T);
+            const uint32_t q = (uint32_t)__ldg(qb + ((long long)g * a.n_rounds + n) * pg.T);
             if (q > 65535u) continue;  // no tag holds it
             const uint32_t qq = q * 0x10001u;
-            acc += (__vseteq2(u.x, qq) & m0) + (__vseteq2(u.y, qq) & m1) + (__vseteq2(u.z, qq) & m2) +
-                   (__vseteq2(u.w, qq) & m3);
+            acc += (~differ2(u.x, qq) & m0) + (~differ2(u.y, qq) & m1) + (~differ2(u.z, qq) & m2) +
+                   (~differ2(u.w, qq) & m3);
           }
         }
       }
-      // halves hold at most 4 * G per chunk; the sum of a lane stays below 2^16 (checked on the host)
-      score = (int)__reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
+      // a lane's halves stay below 2^16 (checked on the host)
+      const int sum = __reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
+      if (lane == i) score = sum;
     }
-    if (lane == 0) a.scores[(bh * pg.T + t) * pg.max_pages + lp] = score;
+    if (has) a.scores[((long long)bh * pg.T + t) * pg.max_pages + mine] = score;
   }
 }
 
-// Sum over the block; every thread gets it.
+// Maximum and sum over the block; every thread gets them.
 __device__ __forceinline__ int block_max(int v, int* red) {
   v = __reduce_max_sync(0xffffffffu, v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -139,7 +188,7 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectAr
     if (block_count(cnt, red) >= want) lo = mid; else hi = mid;
   }
   // a thread's stretch of pages: how many score above lo, how many equal it
-  const int per = (n_free + kPickThreads - 1) / kPickThreads;
+  const int per = ((n_free + kPickThreads - 1) / kPickThreads) | 1;  // odd: no shared-memory bank conflicts
   const int i0 = min((int)threadIdx.x * per, n_free), i1 = min(i0 + per, n_free);
   int above = 0, equal = 0;
   for (int i = i0; i < i1; ++i) {
