@@ -380,7 +380,7 @@ LSH_API lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int
                                     int mask, int32_t* selected, int32_t* scores, void* stream);
 
 /*
- * Bytes of scratch that lsh_cache_attend needs for these sizes (0 for sizes it does not take);
+ * Bytes of scratch that lsh_cache_attend needs for these sizes (0 when none, as for short contexts);
  * n_select 0 without selection.
  */
 LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, int D, int max_pages, int page,
@@ -401,7 +401,7 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *   out        [B, Hq, T, D] out_dtype     out: softmax-weighted stored values; 0 for padding
  *                                          and rows without an admissible key
  *   lse        [B, Hq, T] float            out: log-sum-exp of the logits; -inf for those
- *   workspace  device scratch of at least lsh_cache_attend_workspace_bytes(...) bytes (never 0),
+ *   workspace  device scratch of at least lsh_cache_attend_workspace_bytes(...) bytes,
  *              contents undefined on entry and on exit; calls that may overlap on the GPU
  *              (other streams, graphs replayed at the same time) need one each
  *

@@ -307,9 +307,11 @@ def lsh_chunk_attend_backward(qk, v, perm, chunk, out, lse, dout, *, self_mask=T
 
 def _fit(t, name, dtype, shape, dev):
     """``_need`` and the device, with one cheap test where all is well; returns the data pointer."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
-            and t.is_contiguous() and t.is_cuda):
-        return t.data_ptr()
+    try:
+        if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():  # (dev is a CUDA device)
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _need(t, name, dtype, shape)
     raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
@@ -367,11 +369,10 @@ def _need_cache(cache, D, page, group):
 
 def _need_pages(page_table, ctx_len, new_len, dev):
     """(B, max_pages, the three pointers)."""
-    _need(page_table, "page_table", torch.int32)
-    shape = page_table.shape
-    if len(shape) != 2:
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    lengths = (shape[0],)
+    shape = page_table.shape
+    lengths = shape[:1]
     return (shape[0], shape[1], _fit(page_table, "page_table", torch.int32, shape, dev),
             _fit(ctx_len, "ctx_len", torch.int32, lengths, dev),
             None if new_len is None else _fit(new_len, "new_len", torch.int32, lengths, dev))
@@ -512,11 +513,14 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
         raise ValueError(f"unsupported dtype {out_dtype}")
     out, op = _new(out, "out", out_dtype, shape, q)
     lse, lp = _new(lse, "lse", torch.float32, shape[:3], q)
+    ws, nbytes = None, 0
     if workspace is None:
-        need = _attend_workspace(dt, B, Hq, H, T, D, max_pages, page, n_select, dev.index)
-        workspace = q.new_empty(max(need, 16), dtype=torch.uint8)
-    nbytes = workspace.numel()
-    ws = _fit(workspace, "workspace", torch.uint8, workspace.shape, dev)
+        nbytes = _attend_workspace(dt, B, Hq, H, T, D, max_pages, page, n_select, dev.index)
+        if nbytes:
+            workspace = q.new_empty(nbytes, dtype=torch.uint8)
+            ws = workspace.data_ptr()
+    else:
+        ws, nbytes = _fit(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
     _on_device(dev, stream, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D,
                _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, ctx, new, table, max_pages, page, group, sel,
                n_select, (1 if self_mask else 0) | (2 if causal else 0), 1 if unit_keys else 0,

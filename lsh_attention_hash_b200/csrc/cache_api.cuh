@@ -59,6 +59,7 @@ lsh_status cache_form_dispatch(int D, int group, Fn f) {
 struct AttendPlan {
   long long units, blocks;  // (cached head [, row]) of all sequences; blocks of all items with full tables
   int cols, cw, nt, n_ct, max_ctas;
+  bool direct;  // one CTA per item, no workspace
 };
 
 constexpr int kMaxCtasPerSm = 6;
@@ -75,6 +76,7 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
   p.nt = p.cols <= 4 ? 1 : p.cols <= 8 ? 2 : most;
   p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
   const long long keys = (long long)(sel ? n_select : max_pages) * page;
+  p.direct = keys <= 1024;
   const int block = lsh::cache::kBlockTiles * lsh::cache::kTileTokens;
   p.blocks = p.units * p.n_ct * ((keys + block - 1) / block);
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
@@ -84,6 +86,7 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
 
 // Two pieces per CTA: unnormalised outputs, then (maximum, sum).
 inline size_t attend_plan_bytes(const AttendPlan& p, int D) {
+  if (p.direct) return 0;
   const size_t n = (size_t)p.max_ctas * 2 * p.cw * p.nt;
   return n * D * sizeof(float) + n * 2 * sizeof(float);
 }
@@ -109,9 +112,11 @@ lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, c
   if (st != LSH_OK) return st;
   static_assert(C::kCtas >= 1 && C::kCtas <= kMaxCtasPerSm, "workspace is sized for it");
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
-  a.nc = std::min(p.max_ctas, sms * C::kCtas);
+  a.direct = p.direct;
+  a.nc = p.direct ? (int)(p.units * p.n_ct) : std::min(p.max_ctas, sms * C::kCtas);
   kfn<<<a.nc, kAttThreads, C::kSmem, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
+  if (p.direct) return LSH_OK;
   // the join may be set up while the last CTAs run; it waits for them before it reads
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.units * p.cols));
@@ -237,11 +242,18 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
   a.causal = (mask & LSH_MASK_CAUSAL) ? 1 : 0;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   cudaStream_t s = as_stream(stream);
-  const int groups = (max_pages + lsh::cache::kWarpPages - 1) / lsh::cache::kWarpPages;
   const int per = lsh::cache::kScoreThreads / 32;
-  const long long ctas = ((long long)B * H * groups + per - 1) / per;
-  if (ctas > 0) {
-    const unsigned grid = (unsigned)ctas;
+  // up to 64 KB of tags a head: the CTA that picks scores them itself (8 heads of 4093 tokens in 4 rounds:
+  // SELECT_TWO us as two kernels, SELECT_ONE us as one)
+  const bool fused = (long long)max_pages * page * n_rounds * 2 <= 64 * 1024;
+  if (!fused && max_pages > 0) {
+    // pages a warp: eight, fewer where that would leave the device with less than 16 warps an SM
+    const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
+    int wp = lsh::cache::kWarpPages;
+    while (wp > 1 && (long long)B * H * max_pages / wp < 16ll * sms) wp /= 2;
+    a.warp_pages = wp;
+    const int groups = (max_pages + wp - 1) / wp;
+    const unsigned grid = (unsigned)(((long long)B * H * groups + per - 1) / per);
     const int threads = lsh::cache::kScoreThreads;
     // a lane's chunks of a page in registers for one query head and up to 8 rounds of 128 tokens
     const int chunks = a.G == 1 && n_rounds * page % 256 == 0 ? n_rounds * page / 256 : 0;
@@ -250,7 +262,8 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
     else if (chunks == 4) lsh::cache::cache_score_kernel<4><<<grid, threads, 0, s>>>(a, groups);
     else lsh::cache::cache_score_kernel<0><<<grid, threads, 0, s>>>(a, groups);
   }
-  const int smem = max_pages > n_select ? max_pages * 4 : 16;
+  const int smem = fused || max_pages > n_select ? std::max(16, max_pages * 4) : 16;
+  a.fused = fused;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(lsh::cache::cache_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess)
@@ -289,8 +302,8 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   const AttendPlan p = attend_plan(dtype, B, H, Hq / H, T, D, max_pages, page, n_select);
   if (p.units * p.cols >= (1ll << 31) || p.units * p.n_ct >= (1ll << 31)) return LSH_ERR_SHAPE;
   const size_t need = attend_plan_bytes(p, D);
-  if (!workspace || workspace_bytes < need) return LSH_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return LSH_ERR_ALIGN;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return LSH_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return LSH_ERR_ALIGN;
   if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)D);
   lsh::cache::AttendArgs a;
   a.q = q;
@@ -299,7 +312,7 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   a.out = out;
   a.lse = lse;
   a.part_o = static_cast<float*>(workspace);
-  a.part_ml = a.part_o + (size_t)p.max_ctas * 2 * p.cw * p.nt * D;
+  a.part_ml = need ? a.part_o + (size_t)p.max_ctas * 2 * p.cw * p.nt * D : nullptr;
   a.B = B;
   a.G = Hq / H;
   a.n_select = n_select;

@@ -41,7 +41,9 @@
 // selected, each of ceil(keys / 128) blocks; CTA c of NC takes blocks [c W / NC, (c + 1) W / NC) of
 // it, whatever the lengths are, so one wave of CTAs ends together.  An item inside one CTA is
 // written out there; the pieces of any other go to the workspace (a CTA has two at most: its
-// first and its last) and the join adds them up in order.
+// first and its last) and the join adds them up in order.  Where no item has more than 1024 keys,
+// each has a CTA to itself and there is nothing to join (8 heads of 1021 keys: 8.9 us with two
+// kernels, KERNEL_DIRECT us with one).
 #pragma once
 
 #include <type_traits>
@@ -68,6 +70,7 @@ struct AttendArgs {
   int B, G, n_select;
   int causal, self_mask, unit_keys, out_f32;
   float scale_log2;         // scale * log2(e)
+  int direct;               // one CTA per item (short key lists): no pieces, no join
   int nc, n_ct, cols, tile_cols;  // CTAs; column tiles, all columns, columns of a tile
   Pages pg;
 };
@@ -261,28 +264,58 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   int slot = 0;
   uint32_t phase = 0;
 
-  // the join may be set up (it waits for this kernel's end before it reads): every CTA is resident
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   // ---- the CTA's stretch of the work -----------------------------------------------------------------
-  long long total, before;
-  work_before(a, 0, lane, total, before);
-  const long long nc = min((long long)a.nc, total);  // CTAs with work: a block each at least
-  if (blockIdx.x >= nc) return;
-  long long x = blockIdx.x * total / nc;
-  const long long x_end = (blockIdx.x + 1) * total / nc;
-  int b = work_find(a, x, lane, before);
-  Seq u = seq_of(a, b);
+  long long before = 0, x = 0, x_end = 1;
+  int b, own_item = 0;
+  Seq u;
+  if (a.direct) {
+    const int unit = blockIdx.x / a.n_ct, ct = blockIdx.x - unit * a.n_ct;
+    const int bh = sel ? unit / a.pg.T : unit, t = sel ? unit - bh * a.pg.T : 0;
+    b = bh / a.pg.H;
+    const int h = bh - b * a.pg.H;
+    u = seq_of(a, b);
+    if (u.n_rows == 0 || (sel && !row_live(u, t))) {  // padding: zeros
+      const int col0 = ct * C::kQ, n = min(C::kQ, a.cols - col0);
+      for (int i = tid; i < n * D; i += kAttThreads) {
+        const int col = col0 + i / D, d = i % D;
+        const int tt = sel ? t : col / a.G, gg = sel ? col : col - tt * a.G;
+        const long long row = ((long long)bh * a.G + gg) * a.pg.T + tt;
+        if (a.out_f32)
+          static_cast<float*>(a.out)[row * D + d] = 0.f;
+        else
+          static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16_rn(0.f);
+        if (d == 0) a.lse[row] = -INFINITY;
+      }
+      return;
+    }
+    own_item = (sel ? h * u.n_rows + t - u.row0 : h) * a.n_ct + ct;
+  } else {
+    // the join may be set up (it waits for this kernel's end before it reads): every CTA is resident
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    long long total;
+    work_before(a, 0, lane, total, before);
+    const long long nc = min((long long)a.nc, total);  // CTAs with work: a block each at least
+    if (blockIdx.x >= nc) return;
+    x = blockIdx.x * total / nc;
+    x_end = (blockIdx.x + 1) * total / nc;
+    b = work_find(a, x, lane, before);
+    u = seq_of(a, b);
+  }
 
   while (x < x_end) {
-  while (x >= before + (long long)u.items * u.nb) {  // the next sequence with anything to do
-    before += (long long)u.items * u.nb;
-    u = seq_of(a, ++b);
+  int item = own_item, blk0 = 0, blk1 = u.nb;
+  if (a.direct) {
+    x = x_end;
+  } else {
+    while (x >= before + (long long)u.items * u.nb) {  // the next sequence with anything to do
+      before += (long long)u.items * u.nb;
+      u = seq_of(a, ++b);
+    }
+    item = (int)((x - before) / u.nb);
+    blk0 = (int)((x - before) - (long long)item * u.nb);
+    blk1 = (int)min((long long)u.nb, blk0 + (x_end - x));
+    x += blk1 - blk0;
   }
-  const int item = (int)((x - before) / u.nb);
-  const int blk0 = (int)((x - before) - (long long)item * u.nb);
-  const int blk1 = (int)min((long long)u.nb, blk0 + (x_end - x));
-  x += blk1 - blk0;
   const int ct = item % a.n_ct, rest = item / a.n_ct;
   const int row_t = sel ? u.row0 + rest % u.n_rows : 0;  // the row, with selection
   const int h = sel ? rest / u.n_rows : rest;

@@ -20,7 +20,7 @@ namespace lsh {
 namespace cache {
 
 constexpr int kScoreThreads = 256;
-constexpr int kWarpPages = 8;  // pages of a warp
+constexpr int kWarpPages = 8;  // most pages of a warp
 constexpr int kPickThreads = 512;
 constexpr int kMaxPickPages = 49152;  // scores of one row in shared memory (192 KB)
 
@@ -30,6 +30,7 @@ struct SelectArgs {
   int32_t* scores;           // [B, H, T, max_pages]
   int32_t* selected;         // [B, H, T, n_select]
   int B, G, n_rounds, n_select, n_local, causal;
+  int warp_pages, fused;     // pages of a scoring warp; the picking CTA scores its row itself
   Pages pg;
 };
 
@@ -45,22 +46,49 @@ __device__ __forceinline__ uint32_t differ2(uint32_t tags, uint32_t q2) {
   return __vminu2(tags ^ q2, 0x00010001u);
 }
 
+// Score of one page (whole warp): any sizes, query heads, and a limit inside the page.  ph < 0: missing.
+__device__ __forceinline__ int page_score(const SelectArgs& a, const int32_t* qb, int ph, int h, int first, int limit,
+                                          int lane) {
+  const int cl = a.pg.page_log2 - 3;  // log2 of the 16-byte chunks of a round
+  const int n_chunks = ph >= 0 ? a.n_rounds << cl : 0;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      a.tags + ((((long long)max(ph, 0) * a.pg.H + h) * a.n_rounds) << a.pg.page_log2));
+  uint32_t acc = 0;
+  for (int c = lane; c < n_chunks; c += 32) {
+    const uint4 u = __ldg(src + c);
+    const int n = c >> cl;
+    const int ok = limit - first - ((c & ((1 << cl) - 1)) << 3);  // admissible tokens of the chunk
+    const uint32_t m0 = ok >= 2 ? 0x10001u : (ok == 1 ? 1u : 0u);
+    const uint32_t m1 = ok >= 4 ? 0x10001u : (ok == 3 ? 1u : 0u);
+    const uint32_t m2 = ok >= 6 ? 0x10001u : (ok == 5 ? 1u : 0u);
+    const uint32_t m3 = ok >= 8 ? 0x10001u : (ok == 7 ? 1u : 0u);
+    for (int g = 0; g < a.G; ++g) {
+      const uint32_t q = (uint32_t)__ldg(qb + ((long long)g * a.n_rounds + n) * a.pg.T);
+      if (q > 65535u) continue;  // no tag holds it
+      const uint32_t qq = q * 0x10001u;
+      acc += (~differ2(u.x, qq) & m0) + (~differ2(u.y, qq) & m1) + (~differ2(u.z, qq) & m2) +
+             (~differ2(u.w, qq) & m3);
+    }
+  }
+  // a lane's halves stay below 2^16 (checked on the host)
+  return (int)__reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
+}
+
 // NC: 16-byte chunks of a page per lane (n_rounds * page / 256) when the page is whole and there is one
 // query head, so that the lane's buckets stay in registers; 0: any number.
 template <int NC>
 __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectArgs a, int groups) {
   const int lane = threadIdx.x & 31;
   const Pages& pg = a.pg;
-  const unsigned w = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);  // (head, 8 pages)
+  const unsigned w = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);  // (head, its pages)
   const unsigned bh = w / groups;
   if (bh >= (unsigned)(a.B * pg.H)) return;
-  const int lp0 = (int)(w - bh * groups) * kWarpPages;
+  const int lp0 = (int)(w - bh * groups) * a.warp_pages;
   const int b = bh / pg.H, h = bh - b * pg.H;
   const int page = 1 << pg.page_log2;
   const int cl = pg.page_log2 - 3;  // log2 of the 16-byte chunks of a round
-  const int n_chunks = a.n_rounds << cl;
-  const int mine = lp0 + lane;      // lanes 0..7 have a page each
-  const bool has = lane < kWarpPages && mine < pg.max_pages;
+  const int mine = lp0 + lane;      // the first lanes have a page each
+  const bool has = lane < a.warp_pages && mine < pg.max_pages;
   int phys = -2;                    // of the lane's page, once it is wanted
   const long long row_bytes = (long long)a.n_rounds * page * 2;
   for (int t = 0; t < pg.T; ++t) {
@@ -68,7 +96,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
     if (has && phys == -2 && (mine << pg.page_log2) < limit) phys = page_of(pg, b, mine);
     const int32_t* qb = a.q_buckets + ((long long)bh * a.G * a.n_rounds) * pg.T + t;
     int score = has && (mine << pg.page_log2) < limit ? 0 : -1;
-    const int whole = min(kWarpPages, max(0, (limit >> pg.page_log2) - lp0));  // pages below the limit
+    const int whole = min(a.warp_pages, max(0, (limit >> pg.page_log2) - lp0));  // pages below the limit
     int i = 0;
     if (NC > 0) {
       uint32_t q2[NC > 0 ? NC : 1];
@@ -101,32 +129,9 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
       }
     }
     // the page that the limit cuts, other sizes, several query heads
-    for (; i < kWarpPages && ((lp0 + i) << pg.page_log2) < limit; ++i) {
+    for (; i < a.warp_pages && ((lp0 + i) << pg.page_log2) < limit; ++i) {
       const int ph = __shfl_sync(0xffffffffu, phys, i);
-      const int first = (lp0 + i) << pg.page_log2;
-      uint32_t acc = 0;
-      if (ph >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.tags) +
-                                                          ((long long)ph * pg.H + h) * row_bytes);
-        for (int c = lane; c < n_chunks; c += 32) {
-          const uint4 u = __ldg(src + c);
-          const int n = c >> cl;
-          const int ok = limit - first - ((c & ((1 << cl) - 1)) << 3);  // admissible tokens of the chunk
-          const uint32_t m0 = ok >= 2 ? 0x10001u : (ok == 1 ? 1u : 0u);
-          const uint32_t m1 = ok >= 4 ? 0x10001u : (ok == 3 ? 1u : 0u);
-          const uint32_t m2 = ok >= 6 ? 0x10001u : (ok == 5 ? 1u : 0u);
-          const uint32_t m3 = ok >= 8 ? 0x10001u : (ok == 7 ? 1u : 0u);
-          for (int g = 0; g < a.G; ++g) {
-            const uint32_t q = (uint32_t)__ldg(qb + ((long long)g * a.n_rounds + n) * pg.T);
-            if (q > 65535u) continue;  // no tag holds it
-            const uint32_t qq = q * 0x10001u;
-            acc += (~differ2(u.x, qq) & m0) + (~differ2(u.y, qq) & m1) + (~differ2(u.z, qq) & m2) +
-                   (~differ2(u.w, qq) & m3);
-          }
-        }
-      }
-      // a lane's halves stay below 2^16 (checked on the host)
-      const int sum = __reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
+      const int sum = page_score(a, qb, ph, h, (lp0 + i) << pg.page_log2, limit, lane);
       if (lane == i) score = sum;
     }
     if (has) a.scores[((long long)bh * pg.T + t) * pg.max_pages + mine] = score;
@@ -165,6 +170,19 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectAr
   const int limit = select_limit(a, b, t);
   const int n = limit > 0 ? ((limit - 1) >> pg.page_log2) + 1 : 0;  // candidate pages
   int32_t* out = a.selected + row * a.n_select;
+  if (a.fused) {  // the row's scores: every warp a page at a time
+    const long long bh = row / pg.T;
+    const int h = (int)(bh % pg.H), lane = threadIdx.x & 31;
+    const int32_t* qb = a.q_buckets + bh * a.G * a.n_rounds * pg.T + t;
+    for (int i = threadIdx.x >> 5; i < pg.max_pages; i += kPickThreads / 32) {
+      int score = -1;
+      if (i < n) score = page_score(a, qb, page_of(pg, b, i), h, i << pg.page_log2, limit, lane);
+      if (lane == 0) {
+        a.scores[row * pg.max_pages + i] = score;
+        sc[i] = score;
+      }
+    }
+  }
   if (n <= a.n_select) {
     for (int i = threadIdx.x; i < a.n_select; i += kPickThreads) out[i] = i < n ? i : -1;
     return;
@@ -172,8 +190,9 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectAr
   const int n_free = n - a.n_local;          // pages that the score decides about
   const int want = a.n_select - a.n_local;   // of which so many get in (want < n_free)
   int best = 0;
+  if (a.fused) __syncthreads();
   for (int i = threadIdx.x; i < n_free; i += kPickThreads) {
-    const int s = a.scores[row * pg.max_pages + i];
+    const int s = a.fused ? sc[i] : a.scores[row * pg.max_pages + i];
     sc[i] = s;
     best = max(best, s);
   }
