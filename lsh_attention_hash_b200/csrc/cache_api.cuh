@@ -159,15 +159,15 @@ lsh_status lsh_cache_write(const void* k, const void* v, int dtype, int B, int H
   a.buckets = buckets;
   a.cache = static_cast<uint8_t*>(cache);
   a.tags = tags;
-  a.rows = (long long)B * H * T;
+  a.rows = (unsigned)B * H * T;
   a.n_rounds = n_rounds;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   if (a.rows == 0 || max_pages == 0) return LSH_OK;
   cudaStream_t s = as_stream(stream);
   return cache_form_dispatch(D, group, [&](auto DC, auto GC) {
     constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
-    const long long threads = a.rows * (DD / 8);
-    const unsigned grid = (unsigned)((threads + lsh::cache::kRwThreads - 1) / lsh::cache::kRwThreads);
+    const unsigned per = lsh::cache::kRwThreads / (DD / 16);  // rows of a CTA
+    const unsigned grid = (a.rows + per - 1) / per;
     if (dtype == LSH_F32)
       lsh::cache::cache_write_kernel<float, DD, GG><<<grid, lsh::cache::kRwThreads, 0, s>>>(a);
     else
@@ -192,14 +192,14 @@ lsh_status lsh_cache_read(const void* cache, int n_pages, int B, int H, int T, i
   a.k = k;
   a.v = v;
   a.inv = key_inv;
-  a.rows = (long long)B * H * T;
+  a.rows = (unsigned)B * H * T;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   if (a.rows == 0) return LSH_OK;
   cudaStream_t s = as_stream(stream);
   return cache_form_dispatch(D, group, [&](auto DC, auto GC) {
     constexpr int DD = decltype(DC)::value, GG = decltype(GC)::value;
-    const long long threads = a.rows * (DD / 8);
-    const unsigned grid = (unsigned)((threads + lsh::cache::kRwThreads - 1) / lsh::cache::kRwThreads);
+    const unsigned per = lsh::cache::kRwThreads / (DD / 16);  // rows of a CTA
+    const unsigned grid = (a.rows + per - 1) / per;
     if (out_dtype == LSH_F32)
       lsh::cache::cache_read_kernel<float, DD, GG><<<grid, lsh::cache::kRwThreads, 0, s>>>(a);
     else

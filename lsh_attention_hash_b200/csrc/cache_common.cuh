@@ -95,17 +95,6 @@ __device__ __forceinline__ uint32_t transpose_bytes4(uint32_t x, int lane) {
   return __byte_perm(x, y, (lane & 1) ? 0x3715 : 0x6240);
 }
 
-// 8 x 8 nibble transpose over 8 neighbouring lanes: nibble n of lane i becomes nibble i of lane n.
-__device__ __forceinline__ uint32_t transpose_nibbles8(uint32_t x, int lane) {
-  uint32_t y = __shfl_xor_sync(0xffffffffu, x, 4);
-  x = __byte_perm(x, y, (lane & 4) ? 0x3276 : 0x5410);
-  y = __shfl_xor_sync(0xffffffffu, x, 2);
-  x = __byte_perm(x, y, (lane & 2) ? 0x3715 : 0x6240);
-  y = __shfl_xor_sync(0xffffffffu, x, 1);
-  return (lane & 1) ? ((y >> 4) & 0x0f0f0f0fu) | (x & 0xf0f0f0f0u)
-                    : (x & 0x0f0f0f0fu) | ((y & 0x0f0f0f0fu) << 4);
-}
-
 __device__ __forceinline__ float bf16_bits(uint32_t b) { return __uint_as_float(b << 16); }
 
 }  // namespace cache

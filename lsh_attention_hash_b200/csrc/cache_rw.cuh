@@ -9,8 +9,12 @@
 // quotient that lies so near a border that its rounding could decide is settled by
 // the exact remainder, so a code depends on nothing but its inputs.
 //
-// D/8 lanes own a row, 8 dims each (one 16-byte load in bf16); the codes change
-// lanes by a byte transpose (K) and a nibble transpose (V) and leave as whole words.
+// No clamp to 15 is needed: s is off by 2^-9 of itself at most, so (hi - z) / s <= 15.03.
+//
+// D/16 lanes own a row, 16 dims each of K and of V; the codes change lanes by one (K) and four
+// (V) shuffles and leave as whole words.  Both kernels are streams bound by instruction issue
+// before they are bound by memory, so a code costs few: the three-input minimum and maximum of
+// sm_100, the integer taken from a float's mantissa, packing by multiply-add.
 #pragma once
 
 #include "cache_common.cuh"
@@ -36,8 +40,20 @@ __device__ __forceinline__ float floor_bf16(float x) {
   return __uint_as_float(t);
 }
 
+// Minimum and maximum of three; a NaN stays.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Scale of a group from hi - z (see above); s = NaN when the group holds a non-finite value or its
-// range overflows.  lo is -inf for a group with a NaN.
+// range overflows (lo and hi are NaN for a group with a NaN).
 __device__ __forceinline__ GroupParams group_params(float lo, float hi) {
   GroupParams g;
   g.z = floor_bf16(lo);
@@ -60,12 +76,13 @@ __device__ __forceinline__ GroupParams group_params(float lo, float hi) {
   return g;
 }
 
-// Code of x; inv = 1 / s, or 0 for a constant or non-finite group.
-__device__ __forceinline__ uint32_t code_of(float x, const GroupParams& g, float inv) {
+// 1.5 * 2^23 plus the code of x: a float whose low mantissa bits are the code.  inv = 1 / s.
+__device__ __forceinline__ float code_of(float x, const GroupParams& g, float inv) {
+  constexpr float kMagic = 12582912.f;
   const float d = x - g.z;
   const float t = d * inv;  // error below 3e-6: 15 * 3 roundings
-  float k = rintf(t);
-  if (fabsf(t - k) > 0.49997f) {
+  float k = t + kMagic;     // ties to even
+  if (fabsf(t - (k - kMagic)) > 0.49997f) {
     // near a border: the sign of x - z - (f + 1/2) s decides, with the rounding of x - z put back
     const float f = floorf(t);
     const float q = (f + 0.5f) * g.s;  // exact: 5 + 8 bits
@@ -73,33 +90,100 @@ __device__ __forceinline__ uint32_t code_of(float x, const GroupParams& g, float
     const float e = (x - (d - bp)) + (-g.z - bp);
     const float r = (d - q) + e;
     const bool odd = (int)f & 1;
-    k = (r > 0.f || (r == 0.f && odd)) ? f + 1.f : f;
+    k = ((r > 0.f || (r == 0.f && odd)) ? f + 1.f : f) + kMagic;
   }
-  return (uint32_t)(int)fminf(k, 15.f);  // NaN (a non-finite group) gives 15; masked by the caller
+  return k;
 }
 
-// Quantises the lane's 8 dims: params of its group and the 8 codes.
+// Quantises the lane's 16 dims: params of its group and the codes, nibble i of w[0] dim i, of w[1] dim 8 + i.
 template <int GROUP>
-__device__ __forceinline__ GroupParams quantise8(const float (&x)[8], uint32_t (&c)[8]) {
-  float lo = x[0], hi = x[0], poison = 0.f;
+__device__ __forceinline__ GroupParams quantise16(const float (&x)[16], uint32_t (&w)[2]) {
+  float lo = min3(x[0], x[1], x[2]), hi = max3(x[0], x[1], x[2]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    poison = fmaf(x[i], 0.f, poison);  // NaN if any x is infinite or NaN
+  for (int i = 3; i < 15; i += 2) {
+    lo = min3(lo, x[i], x[i + 1]);
+    hi = max3(hi, x[i], x[i + 1]);
   }
-  if (poison != 0.f) lo = -INFINITY;
+  lo = min3(lo, x[15], x[15]);
+  hi = max3(hi, x[15], x[15]);
 #pragma unroll
-  for (int o = 1; o < GROUP / 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+  for (int o = 1; o < GROUP / 16; o <<= 1) {
+    const float l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+    lo = min3(lo, l2, l2);
+    hi = max3(hi, h2, h2);
   }
   const GroupParams g = group_params(lo, hi);
   const bool codes = g.s > 0.f;
   const float inv = codes ? 1.f / g.s : 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = codes ? code_of(x[i], g, inv) : 0u;
+  for (int j = 0; j < 2; ++j) {
+    // sum of (0x4B400000 + code) 16^i; what the floats' upper bits add up to is taken off again
+    uint32_t sum = 0u - 0x4B400000u * 0x11111111u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += __float_as_uint(code_of(x[8 * j + i], g, inv)) << (4 * i);
+    w[j] = codes ? sum : 0u;
+  }
   return g;
+}
+
+// The codes of 32 (K) or 64 (V) dims between "16 dims of a lane" and "words of the tile" (the same
+// exchange leads back).  K: two lanes; of words t = 0..3 lane `half` has 2 half and 2 half + 1.
+__device__ __forceinline__ void k_to_words(uint32_t (&w)[2], int half) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5410), b = __byte_perm(w[0], w[1], 0x7632);
+  const uint32_t r = __shfl_xor_sync(0xffffffffu, half ? a : b, 1);
+  const uint32_t lo = half ? r : a, hi = half ? b : r;
+  w[0] = __byte_perm(lo, hi, 0x6420);
+  w[1] = __byte_perm(lo, hi, 0x7531);
+}
+__device__ __forceinline__ void words_to_k(uint32_t (&w)[2], int half) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+  const uint32_t r = __shfl_xor_sync(0xffffffffu, half ? a : b, 1);
+  const uint32_t lo = half ? r : a, hi = half ? b : r;
+  w[0] = __byte_perm(lo, hi, 0x5410);
+  w[1] = __byte_perm(lo, hi, 0x7632);
+}
+// V: four lanes; lane u has the words of chunks 2 u and 2 u + 1.
+__device__ __forceinline__ void v_to_words(uint32_t (&w)[2], int lane) {
+  const uint32_t even = (w[0] & 0x0f0f0f0fu) | ((w[1] & 0x0f0f0f0fu) << 4);
+  const uint32_t odd = ((w[0] >> 4) & 0x0f0f0f0fu) | (w[1] & 0xf0f0f0f0u);
+  w[0] = transpose_bytes4(even, lane);
+  w[1] = transpose_bytes4(odd, lane);
+}
+__device__ __forceinline__ void words_to_v(uint32_t (&w)[2], int lane) {
+  const uint32_t even = transpose_bytes4(w[0], lane), odd = transpose_bytes4(w[1], lane);
+  w[0] = (even & 0x0f0f0f0fu) | ((odd & 0x0f0f0f0fu) << 4);
+  w[1] = ((even >> 4) & 0x0f0f0f0fu) | (odd & 0xf0f0f0f0u);
+}
+
+// Offsets in a tile of a lane's two words of K and of V, for token r and dims 16 j .. 16 j + 15.
+template <int D>
+struct LaneWords {
+  int k0, v0, v1;
+  __device__ __forceinline__ LaneWords(int r, int j) {
+    k0 = r * (D / 2) + (j & 1) * 2 * (D / 8) + (j >> 1) * 4;  // the second word D/8 further
+    const int pair = r >> 1, x = 2 * (pair & 3), c = 2 * (j & 3);
+    const int base = 8 * D + pair * D + (j >> 2) * 8 + (r & 1) * 4;
+    v0 = base + (c ^ x) * (D / 8);
+    v1 = base + ((c + 1) ^ x) * (D / 8);
+  }
+};
+
+// A row of the call and its place: (b, h, t) of row = (b H + h) T + t, its position and physical page
+// (-1: padding, or a page that is missing).
+struct Row {
+  int b, h, t, pos, phys;
+  unsigned bh;
+};
+
+__device__ __forceinline__ Row row_of(const Pages& p, unsigned row) {
+  Row r;
+  r.bh = row / (unsigned)p.T;
+  r.t = (int)(row - r.bh * p.T);
+  r.b = (int)(r.bh / (unsigned)p.H);
+  r.h = (int)(r.bh - (unsigned)r.b * p.H);
+  r.pos = row_pos(p, r.b, r.t);
+  r.phys = r.pos >= 0 ? page_of(p, r.b, r.pos >> p.page_log2) : -1;
+  return r;
 }
 
 struct WriteArgs {
@@ -107,7 +191,7 @@ struct WriteArgs {
   const int32_t* buckets;   // [B, H, n_rounds, T] or null
   uint8_t* cache;           // [n_pages, H, block]
   uint16_t* tags;           // [n_pages, H, n_rounds, page] or null
-  long long rows;           // B * H * T
+  unsigned rows;            // B * H * T
   int n_rounds;
   Pages pg;
 };
@@ -115,60 +199,56 @@ struct WriteArgs {
 template <typename T, int D, int GROUP>
 __global__ void __launch_bounds__(kRwThreads) cache_write_kernel(const WriteArgs a) {
   using F = Fmt<D, GROUP>;
-  constexpr int kLanes = D / 8;  // lanes of a row
-  const long long gt = (long long)blockIdx.x * kRwThreads + threadIdx.x;
-  const long long row = gt / kLanes;
-  const int j = (int)(gt % kLanes), lane = threadIdx.x & 31;
-  const bool live = row < a.rows;
-  float xk[8], xv[8];
+  constexpr int kLanes = D / 16;  // lanes of a row
+  const unsigned row = blockIdx.x * (kRwThreads / kLanes) + threadIdx.x / kLanes;
+  const int j = threadIdx.x % kLanes, lane = threadIdx.x & 31;
+  Row r;
+  r.phys = -1;
+  if (row < a.rows) r = row_of(a.pg, row);
+  const bool live = r.phys >= 0;  // of padding nothing is read
+  float x[16];
+  uint32_t wk[2], wv[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) xk[i] = xv[i] = 0.f;
-  int pos = -1, phys = -1, h = 0, b = 0, tok = 0;
-  long long bh = 0;
+  for (int i = 0; i < 16; ++i) x[i] = 0.f;
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = 0.f;
   if (live) {
-    load8(static_cast<const T*>(a.k) + row * D + j * 8, xk);
-    load8(static_cast<const T*>(a.v) + row * D + j * 8, xv);
-    bh = row / a.pg.T;
-    tok = (int)(row - bh * a.pg.T);
-    b = (int)(bh / a.pg.H);
-    h = (int)(bh - (long long)b * a.pg.H);
-    pos = row_pos(a.pg, b, tok);
-    if (pos >= 0) phys = page_of(a.pg, b, pos >> a.pg.page_log2);
+    const long long at = (long long)row * D + j * 16;
+    load8(static_cast<const T*>(a.k) + at, *reinterpret_cast<float(*)[8]>(x));
+    load8(static_cast<const T*>(a.k) + at + 8, *reinterpret_cast<float(*)[8]>(x + 8));
+    load8(static_cast<const T*>(a.v) + at, *reinterpret_cast<float(*)[8]>(y));
+    load8(static_cast<const T*>(a.v) + at + 8, *reinterpret_cast<float(*)[8]>(y + 8));
   }
-  uint32_t ck[8], cv[8];
-  const GroupParams gk = quantise8<GROUP>(xk, ck);
-  const GroupParams gv = quantise8<GROUP>(xv, cv);
+  const GroupParams gk = quantise16<GROUP>(x, wk);
+  const GroupParams gv = quantise16<GROUP>(y, wv);
   float sq = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sq = fmaf(xk[i], xk[i], sq);
+  for (int i = 0; i < 16; ++i) sq = fmaf(x[i], x[i], sq);
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-  uint32_t wk = 0, wv = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wk |= ck[i] << (4 * i);
-    wv |= cv[i] << (4 * i);
+  k_to_words(wk, j & 1);
+  v_to_words(wv, lane);
+  if (!live) return;
+  const int t = r.pos & 15;
+  uint8_t* tile = a.cache + tile_offset(a.pg, r.phys, r.h, r.pos, F::kTile);
+  const LaneWords<D> at(t, j);
+  *reinterpret_cast<uint32_t*>(tile + at.k0) = wk[0];
+  *reinterpret_cast<uint32_t*>(tile + at.k0 + D / 8) = wk[1];
+  *reinterpret_cast<uint32_t*>(tile + at.v0) = wv[0];
+  *reinterpret_cast<uint32_t*>(tile + at.v1) = wv[1];
+  if (j % (GROUP / 16) == 0) {
+    const int grp = j / (GROUP / 16);
+    reinterpret_cast<uint32_t*>(tile + F::kOffKp)[grp * 16 + t] = gk.word;
+    reinterpret_cast<uint32_t*>(tile + F::kOffVp)[grp * 16 + t] = gv.word;
   }
-  wk = transpose_bytes4(wk, lane);
-  wv = transpose_nibbles8(wv, lane);
-  if (phys < 0) return;
-  const int r = pos & 15, pair = r >> 1, e = r & 1;
-  uint8_t* tile = a.cache + tile_offset(a.pg, phys, h, pos, F::kTile);
-  *reinterpret_cast<uint32_t*>(tile + r * (D / 2) + (j & 3) * (D / 8) + (j >> 2) * 4) = wk;
-  *reinterpret_cast<uint32_t*>(tile + F::kOffV + pair * D + ((j & 7) ^ (2 * (pair & 3))) * (D / 8) + (j >> 3) * 8 +
-                               e * 4) = wv;
-  if (j % (GROUP / 8) == 0) {
-    const int grp = j / (GROUP / 8);
-    reinterpret_cast<uint32_t*>(tile + F::kOffKp)[grp * 16 + r] = gk.word;
-    reinterpret_cast<uint32_t*>(tile + F::kOffVp)[grp * 16 + r] = gv.word;
-  }
-  if (j == 0) reinterpret_cast<float*>(tile + F::kOffInv)[r] = 1.f / fmaxf(sqrtf(sq), 1e-12f);
+  if (j == 0) reinterpret_cast<float*>(tile + F::kOffInv)[t] = 1.f / fmaxf(sqrtf(sq), 1e-12f);
   if (a.tags) {
     const int page = 1 << a.pg.page_log2;
     for (int n = j; n < a.n_rounds; n += kLanes) {
-      const int32_t bk = a.buckets[(bh * a.n_rounds + n) * a.pg.T + tok];
+      const int32_t bk = a.buckets[((long long)r.bh * a.n_rounds + n) * a.pg.T + r.t];
       if ((uint32_t)bk > 65535u) record_error(LSH_ERR_INVALID_ARG);
-      a.tags[(((long long)phys * a.pg.H + h) * a.n_rounds + n) * page + (pos & (page - 1))] = (uint16_t)bk;
+      a.tags[(((long long)r.phys * a.pg.H + r.h) * a.n_rounds + n) * page + (r.pos & (page - 1))] = (uint16_t)bk;
     }
   }
 }
@@ -177,49 +257,75 @@ struct ReadArgs {
   const uint8_t* cache;
   void *k, *v;      // [B, H, T, D]
   float* inv;       // [B, H, T] or null
-  long long rows;
+  unsigned rows;
   Pages pg;
 };
+
+// z + s code of the 16 codes, rounded once, to 16 consecutive elements.
+__device__ __forceinline__ void store16(float* p, const uint32_t (&w)[2], uint32_t params) {
+  const float s = bf16_bits(params & 0xffffu), z = __uint_as_float(params & 0xffff0000u);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = fmaf(s, __uint_as_float(((w[j] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f, z);
+    store8(p + 8 * j, x);
+  }
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&w)[2], uint32_t params) {
+  const uint32_t s2 = __byte_perm(params, 0, 0x1010), z2 = __byte_perm(params, 0, 0x3232);
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2), z = *reinterpret_cast<const __nv_bfloat162*>(&z2);
+  const uint32_t c128 = 0x43004300u;  // 0x4300 | code is 128 + code in bf16
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t y[4];  // dims i and i + 4
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = ((w[j] >> (4 * i)) & 0x000f000fu) | c128;
+      const __nv_bfloat162 v = __hfma2(s, __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c),
+                                                  *reinterpret_cast<const __nv_bfloat162*>(&c128)), z);
+      y[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint4 u;
+    u.x = __byte_perm(y[0], y[1], 0x5410);
+    u.y = __byte_perm(y[2], y[3], 0x5410);
+    u.z = __byte_perm(y[0], y[1], 0x7632);
+    u.w = __byte_perm(y[2], y[3], 0x7632);
+    *reinterpret_cast<uint4*>(p + 8 * j) = u;
+  }
+}
 
 template <typename T, int D, int GROUP>
 __global__ void __launch_bounds__(kRwThreads) cache_read_kernel(const ReadArgs a) {
   using F = Fmt<D, GROUP>;
-  constexpr int kLanes = D / 8;
-  const long long gt = (long long)blockIdx.x * kRwThreads + threadIdx.x;
-  const long long row = gt / kLanes;
-  const int j = (int)(gt % kLanes), lane = threadIdx.x & 31;
+  constexpr int kLanes = D / 16;
+  const unsigned row = blockIdx.x * (kRwThreads / kLanes) + threadIdx.x / kLanes;
+  const int j = threadIdx.x % kLanes, lane = threadIdx.x & 31;
   const bool live = row < a.rows;
-  uint32_t wk = 0, wv = 0, pk = 0, pv = 0;
+  uint32_t wk[2] = {0u, 0u}, wv[2] = {0u, 0u}, pk = 0, pv = 0;
   float inv = 0.f;
   if (live) {
-    const long long bh = row / a.pg.T;
-    const int tok = (int)(row - bh * a.pg.T);
-    const int b = (int)(bh / a.pg.H), h = (int)(bh - (long long)b * a.pg.H);
-    const int pos = row_pos(a.pg, b, tok);
-    const int phys = pos >= 0 ? page_of(a.pg, b, pos >> a.pg.page_log2) : -1;
-    if (phys >= 0) {
-      const int r = pos & 15, pair = r >> 1, e = r & 1, grp = j / (GROUP / 8);
-      const uint8_t* tile = a.cache + tile_offset(a.pg, phys, h, pos, F::kTile);
-      wk = *reinterpret_cast<const uint32_t*>(tile + r * (D / 2) + (j & 3) * (D / 8) + (j >> 2) * 4);
-      wv = *reinterpret_cast<const uint32_t*>(tile + F::kOffV + pair * D + ((j & 7) ^ (2 * (pair & 3))) * (D / 8) +
-                                              (j >> 3) * 8 + e * 4);
-      pk = reinterpret_cast<const uint32_t*>(tile + F::kOffKp)[grp * 16 + r];
-      pv = reinterpret_cast<const uint32_t*>(tile + F::kOffVp)[grp * 16 + r];
-      inv = reinterpret_cast<const float*>(tile + F::kOffInv)[r];
+    const Row r = row_of(a.pg, row);
+    if (r.phys >= 0) {
+      const int t = r.pos & 15, grp = j / (GROUP / 16);
+      const uint8_t* tile = a.cache + tile_offset(a.pg, r.phys, r.h, r.pos, F::kTile);
+      const LaneWords<D> at(t, j);
+      wk[0] = *reinterpret_cast<const uint32_t*>(tile + at.k0);
+      wk[1] = *reinterpret_cast<const uint32_t*>(tile + at.k0 + D / 8);
+      wv[0] = *reinterpret_cast<const uint32_t*>(tile + at.v0);
+      wv[1] = *reinterpret_cast<const uint32_t*>(tile + at.v1);
+      pk = reinterpret_cast<const uint32_t*>(tile + F::kOffKp)[grp * 16 + t];
+      pv = reinterpret_cast<const uint32_t*>(tile + F::kOffVp)[grp * 16 + t];
+      inv = reinterpret_cast<const float*>(tile + F::kOffInv)[t];
     }
   }
-  wk = transpose_bytes4(wk, lane);
-  wv = transpose_nibbles8(wv, lane);
+  words_to_k(wk, j & 1);
+  words_to_v(wv, lane);
   if (!live) return;
-  const float sk = bf16_bits(pk & 0xffffu), zk = __uint_as_float(pk & 0xffff0000u);
-  const float sv = bf16_bits(pv & 0xffffu), zv = __uint_as_float(pv & 0xffff0000u);
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(sk, (float)((wk >> (4 * i)) & 15u), zk);
-  store8(static_cast<T*>(a.k) + row * D + j * 8, x);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(sv, (float)((wv >> (4 * i)) & 15u), zv);
-  store8(static_cast<T*>(a.v) + row * D + j * 8, x);
+  const long long at = (long long)row * D + j * 16;
+  store16(static_cast<T*>(a.k) + at, wk, pk);
+  store16(static_cast<T*>(a.v) + at, wv, pv);
   if (a.inv && j == 0) a.inv[row] = inv;
 }
 
