@@ -36,6 +36,8 @@ inline lsh::cache::Pages pages_of(const int32_t* table, const int32_t* ctx_len, 
   p.n_pages = n_pages;
   p.H = H;
   p.T = T;
+  p.div_t = lsh::cache::FastDiv::by((uint32_t)T);
+  p.div_h = lsh::cache::FastDiv::by((uint32_t)H);
   return p;
 }
 

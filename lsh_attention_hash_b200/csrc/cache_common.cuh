@@ -40,12 +40,28 @@ struct Fmt {
 
 __host__ __device__ constexpr int tile_bytes(int D, int group) { return 16 * D + 128 * (D / group) + 64; }
 
+// Division of numbers below 2^31 by a fixed one: n / d = (n m) >> (32 + s) with s = ceil(log2 d) - 1 (0 for
+// d = 1) and m = ceil(2^(32 + s) / d), which fits 32 bits for d > 1; the error n / 2^(32 + s) of
+// the rounded-up m stays below 1 / d.
+struct FastDiv {
+  uint32_t m, s;
+  __host__ static FastDiv by(uint32_t d) {
+    FastDiv f{0, 0};
+    if (d <= 1) return f;
+    while ((1ull << (f.s + 1)) < d) ++f.s;
+    f.m = (uint32_t)(((1ull << (32 + f.s)) + d - 1) / d);
+    return f;
+  }
+  __device__ __forceinline__ uint32_t of(uint32_t n) const { return m ? __umulhi(n, m) >> s : n; }
+};
+
 // Where a sequence's pages lie.  Page ids are checked against n_pages at every use.
 struct Pages {
   const int32_t* table;  // [B, max_pages]
   const int32_t* ctx_len;  // [B]
   const int32_t* new_len;  // [B] or null (T for every sequence)
   int max_pages, page_log2, n_pages, H, T;
+  FastDiv div_t, div_h;    // by T and by H
 };
 
 // Tokens of sequence b in the cache.  A count that is negative or more than its table has room

@@ -32,13 +32,14 @@ struct GroupParams {
   uint32_t word;
 };
 
-// The largest bf16 not above x.
-__device__ __forceinline__ float floor_bf16(float x) {
+// The largest bf16 not above x (bf16 rows: x itself).
+__device__ __forceinline__ float floor_bf16(float x, const float*) {
   const uint32_t b = __float_as_uint(x);
   uint32_t t = b & 0xffff0000u;
   if ((b & 0xffffu) && (b >> 31)) t += 0x10000u;
   return __uint_as_float(t);
 }
+__device__ __forceinline__ float floor_bf16(float x, const __nv_bfloat16*) { return x; }
 
 // Minimum and maximum of three; a NaN stays.
 __device__ __forceinline__ float min3(float a, float b, float c) {
@@ -54,20 +55,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // Scale of a group from hi - z (see above); s = NaN when the group holds a non-finite value or its
 // range overflows (lo and hi are NaN for a group with a NaN).
+template <typename T>
 __device__ __forceinline__ GroupParams group_params(float lo, float hi) {
   GroupParams g;
-  g.z = floor_bf16(lo);
+  g.z = floor_bf16(lo, static_cast<const T*>(nullptr));
   const float span = hi - g.z;
-  const float q = span / 15.f;
+  const float q = span * (1.f / 15.f);  // off by 3 units of its last place at most
   uint32_t b = __float_as_uint(q);
-  const uint32_t low = b & 0xffffu;
-  if (low - 0x7ffeu <= 4u) {  // within the float quotient's error of the middle of two bf16
+  if ((b & 0xffffu) - 0x7ffcu <= 8u) {  // the middle of two bf16 is that near: the exact quotient decides
     const double d = (double)hi - (double)g.z;
     const double mid = 15.0 * (double)__uint_as_float((b & 0xffff0000u) | 0x8000u);
     const bool up = d > mid || (d == mid && (b & 0x10000u));
     b = (b & 0xffff0000u) + (up ? 0x10000u : 0u);
   } else {
-    b = (b + 0x7fffu + ((b >> 16) & 1u)) & 0xffff0000u;
+    b = (b + 0x8000u) & 0xffff0000u;
   }
   g.s = __uint_as_float(b);
   if (g.s < kMinScale) g.s = 0.f;
@@ -76,28 +77,82 @@ __device__ __forceinline__ GroupParams group_params(float lo, float hi) {
   return g;
 }
 
-// 1.5 * 2^23 plus the code of x: a float whose low mantissa bits are the code.  inv = 1 / s.
-__device__ __forceinline__ float code_of(float x, const GroupParams& g, float inv) {
-  constexpr float kMagic = 12582912.f;
-  const float d = x - g.z;
-  const float t = d * inv;  // error below 3e-6: 15 * 3 roundings
-  float k = t + kMagic;     // ties to even
-  if (fabsf(t - (k - kMagic)) > 0.49997f) {
-    // near a border: the sign of x - z - (f + 1/2) s decides, with the rounding of x - z put back
-    const float f = floorf(t);
-    const float q = (f + 0.5f) * g.s;  // exact: 5 + 8 bits
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: the low mantissa bits of kMagic + k are k
+
+// kMagic plus the code of x, from the exact remainder at the border next to t = (x - z) / s.
+__device__ __forceinline__ float code_exact(float x, float z, float s, float t) {
+  const float f = floorf(t);
+  if (fabsf(t - f - 0.5f) < 1e-4f) {
+    // the sign of x - z - (f + 1/2) s decides, with the rounding of x - z put back
+    const float d = x - z;
+    const float q = (f + 0.5f) * s;  // exact: 5 + 8 bits
     const float bp = d - x;
-    const float e = (x - (d - bp)) + (-g.z - bp);
+    const float e = (x - (d - bp)) + (-z - bp);
     const float r = (d - q) + e;
     const bool odd = (int)f & 1;
-    k = ((r > 0.f || (r == 0.f && odd)) ? f + 1.f : f) + kMagic;
+    return ((r > 0.f || (r == 0.f && odd)) ? f + 1.f : f) + kMagic;
   }
-  return k;
+  return t + kMagic;
 }
 
-// Quantises the lane's 16 dims: params of its group and the codes, nibble i of w[0] dim i, of w[1] dim 8 + i.
-template <int GROUP>
-__device__ __forceinline__ GroupParams quantise16(const float (&x)[16], uint32_t (&w)[2]) {
+// The 16 codes of a lane as kMagic + code, over x.  s > 0, inv = 1 / s to 2^-22; `rows` is where x came from.
+//
+// t = (x - z) inv is off by 1e-5 at most, so only quotients that near a border are in doubt.
+// fp32: those are rare, found by one comparison for the 16, and settled exactly.  bf16: many values lie
+// exactly on a border.  There one Newton step makes t the nearest float to the quotient, which is
+// k + 1/2 for a true tie and, if x - z is a short number, for nothing else: x, z and s have 8 bits, so
+// only an x or z below 2^-11 s can put the quotient within 2^-20 of a border without being on it (or
+// make x - z inexact).  Such an x lies within 2^-11 of -z / s in codes, so groups where that is
+// near a border, and those with such a z, settle their codes exactly.
+__device__ __forceinline__ void codes16(float (&x)[16], const GroupParams& g, float inv, const float* rows) {
+  float worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float t = (x[i] - g.z) * inv;
+    x[i] = t + kMagic;  // ties to even
+    worst = fmaxf(worst, fabsf(t - (x[i] - kMagic)));
+  }
+  if (worst > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float y = rows[i];
+      x[i] = code_exact(y, g.z, g.s, (y - g.z) * inv);
+    }
+  }
+}
+
+__device__ __forceinline__ void codes16(float (&x)[16], const GroupParams& g, float inv, const __nv_bfloat16*) {
+  const float t0 = -g.z * inv;
+  if (fabsf(t0 - rintf(t0)) > 0.499f || (g.z != 0.f && fabsf(g.z) < g.s * 4.8828125e-4f)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = code_exact(x[i], g.z, g.s, (x[i] - g.z) * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float d = x[i] - g.z;
+      const float t = d * inv;
+      x[i] = fmaf(fmaf(-t, g.s, d), inv, t) + kMagic;
+    }
+  }
+}
+
+// A lane's 16 dims as they lie in memory.
+template <typename T>
+struct Raw {
+  uint4 u[sizeof(T)];
+  __device__ __forceinline__ Raw(const T* p, bool live) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) u[i] = live ? ld16(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+};
+
+// The lane's 16 dims, quantised: params of its group and the codes, nibble i of w[0] dim i, of w[1] dim 8 + i.
+// SQUARES: adds up the squares.
+template <typename T, int GROUP, bool SQUARES>
+__device__ __forceinline__ GroupParams quantise16(const Raw<T>& raw, const T* rows, uint32_t (&w)[2], float& squares) {
+  float x[16];
+  load8(reinterpret_cast<const T*>(raw.u), *reinterpret_cast<float(*)[8]>(x));
+  load8(reinterpret_cast<const T*>(raw.u) + 8, *reinterpret_cast<float(*)[8]>(x + 8));
   float lo = min3(x[0], x[1], x[2]), hi = max3(x[0], x[1], x[2]);
 #pragma unroll
   for (int i = 3; i < 15; i += 2) {
@@ -106,22 +161,31 @@ __device__ __forceinline__ GroupParams quantise16(const float (&x)[16], uint32_t
   }
   lo = min3(lo, x[15], x[15]);
   hi = max3(hi, x[15], x[15]);
+  if (SQUARES) {
+    squares = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) squares = fmaf(x[i], x[i], squares);
+  }
 #pragma unroll
   for (int o = 1; o < GROUP / 16; o <<= 1) {
     const float l2 = __shfl_xor_sync(0xffffffffu, lo, o), h2 = __shfl_xor_sync(0xffffffffu, hi, o);
     lo = min3(lo, l2, l2);
     hi = max3(hi, h2, h2);
   }
-  const GroupParams g = group_params(lo, hi);
-  const bool codes = g.s > 0.f;
-  const float inv = codes ? 1.f / g.s : 0.f;
+  const GroupParams g = group_params<T>(lo, hi);
+  w[0] = w[1] = 0u;
+  if (g.s > 0.f) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(g.s));  // s is 2^-100 .. 2^125
+    codes16(x, g, inv, rows);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    // sum of (0x4B400000 + code) 16^i; what the floats' upper bits add up to is taken off again
-    uint32_t sum = 0u - 0x4B400000u * 0x11111111u;
+    for (int j = 0; j < 2; ++j) {
+      // sum of (0x4B400000 + code) 16^i; what the floats' upper bits add up to is taken off again
+      uint32_t sum = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += __float_as_uint(code_of(x[8 * j + i], g, inv)) << (4 * i);
-    w[j] = codes ? sum : 0u;
+      for (int i = 0; i < 8; ++i) sum = __float_as_uint(x[8 * j + i]) * (1u << (4 * i)) + sum;
+      w[j] = sum;
+    }
   }
   return g;
 }
@@ -177,9 +241,9 @@ struct Row {
 
 __device__ __forceinline__ Row row_of(const Pages& p, unsigned row) {
   Row r;
-  r.bh = row / (unsigned)p.T;
+  r.bh = p.div_t.of(row);
   r.t = (int)(row - r.bh * p.T);
-  r.b = (int)(r.bh / (unsigned)p.H);
+  r.b = (int)p.div_h.of(r.bh);
   r.h = (int)(r.bh - (unsigned)r.b * p.H);
   r.pos = row_pos(p, r.b, r.t);
   r.phys = r.pos >= 0 ? page_of(p, r.b, r.pos >> p.page_log2) : -1;
@@ -197,7 +261,7 @@ struct WriteArgs {
 };
 
 template <typename T, int D, int GROUP>
-__global__ void __launch_bounds__(kRwThreads) cache_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kRwThreads, 4) cache_write_kernel(const WriteArgs a) {
   using F = Fmt<D, GROUP>;
   constexpr int kLanes = D / 16;  // lanes of a row
   const unsigned row = blockIdx.x * (kRwThreads / kLanes) + threadIdx.x / kLanes;
@@ -205,26 +269,14 @@ __global__ void __launch_bounds__(kRwThreads) cache_write_kernel(const WriteArgs
   Row r;
   r.phys = -1;
   if (row < a.rows) r = row_of(a.pg, row);
-  const bool live = r.phys >= 0;  // of padding nothing is read
-  float x[16];
+  const bool live = r.phys >= 0;
   uint32_t wk[2], wv[2];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  float y[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = 0.f;
-  if (live) {
-    const long long at = (long long)row * D + j * 16;
-    load8(static_cast<const T*>(a.k) + at, *reinterpret_cast<float(*)[8]>(x));
-    load8(static_cast<const T*>(a.k) + at + 8, *reinterpret_cast<float(*)[8]>(x + 8));
-    load8(static_cast<const T*>(a.v) + at, *reinterpret_cast<float(*)[8]>(y));
-    load8(static_cast<const T*>(a.v) + at + 8, *reinterpret_cast<float(*)[8]>(y + 8));
-  }
-  const GroupParams gk = quantise16<GROUP>(x, wk);
-  const GroupParams gv = quantise16<GROUP>(y, wv);
-  float sq = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) sq = fmaf(x[i], x[i], sq);
+  const long long from = (long long)row * D + j * 16;
+  float sq, none;
+  const T *k = static_cast<const T*>(a.k) + from, *v = static_cast<const T*>(a.v) + from;
+  const Raw<T> raw_k(k, live), raw_v(v, live);  // of padding nothing is read
+  const GroupParams gk = quantise16<T, GROUP, true>(raw_k, k, wk, sq);
+  const GroupParams gv = quantise16<T, GROUP, false>(raw_v, v, wv, none);
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   k_to_words(wk, j & 1);
