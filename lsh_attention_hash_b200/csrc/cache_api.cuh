@@ -163,6 +163,8 @@ lsh_status lsh_cache_write(const void* k, const void* v, int dtype, int B, int H
   a.tags = tags;
   a.rows = (unsigned)B * H * T;
   a.n_rounds = n_rounds;
+  a.sixteen = 16;
+  a.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   if (a.rows == 0 || max_pages == 0) return LSH_OK;
   cudaStream_t s = as_stream(stream);
@@ -194,6 +196,7 @@ lsh_status lsh_cache_read(const void* cache, int n_pages, int B, int H, int T, i
   a.k = k;
   a.v = v;
   a.inv = key_inv;
+  a.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
   a.rows = (unsigned)B * H * T;
   a.pg = pages_of(page_table, ctx_len, new_len, max_pages, page, n_pages, H, T);
   if (a.rows == 0) return LSH_OK;

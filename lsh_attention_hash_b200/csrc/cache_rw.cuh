@@ -123,7 +123,7 @@ __device__ __forceinline__ void codes16(float (&x)[16], const GroupParams& g, fl
 
 __device__ __forceinline__ void codes16(float (&x)[16], const GroupParams& g, float inv, const __nv_bfloat16*) {
   const float t0 = -g.z * inv;
-  if (fabsf(t0 - rintf(t0)) > 0.499f || (g.z != 0.f && fabsf(g.z) < g.s * 4.8828125e-4f)) {
+  if (fabsf(t0 - ((t0 + kMagic) - kMagic)) > 0.499f || (g.z != 0.f && fabsf(g.z) < g.s * 4.8828125e-4f)) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = code_exact(x[i], g.z, g.s, (x[i] - g.z) * inv);
   } else {
@@ -136,20 +136,49 @@ __device__ __forceinline__ void codes16(float (&x)[16], const GroupParams& g, fl
   }
 }
 
+// 32 bytes (one sector) at a time where the buffers allow it, else 2 x 16: a lane's 16-byte halves of a
+// sector are two requests.
+__device__ __forceinline__ void ld32(uint4 (&u)[2], const void* p, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(u[0].x), "=r"(u[0].y), "=r"(u[0].z), "=r"(u[0].w), "=r"(u[1].x), "=r"(u[1].y), "=r"(u[1].z),
+                   "=r"(u[1].w)
+                 : "l"(p));
+  } else {
+    u[0] = ld16(p);
+    u[1] = ld16(reinterpret_cast<const uint4*>(p) + 1);
+  }
+}
+__device__ __forceinline__ void st32(void* p, const uint4& a, const uint4& b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    st16(p, a);
+    st16(reinterpret_cast<uint4*>(p) + 1, b);
+  }
+}
+
 // A lane's 16 dims as they lie in memory.
 template <typename T>
 struct Raw {
   uint4 u[sizeof(T)];
-  __device__ __forceinline__ Raw(const T* p, bool live) {
+  __device__ __forceinline__ Raw(const T* p, bool live, bool wide) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) u[i] = live ? ld16(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < (int)sizeof(T); ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (live)
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); i += 2)
+        ld32(*reinterpret_cast<uint4(*)[2]>(u + i), reinterpret_cast<const uint4*>(p) + i, wide);
   }
 };
 
 // The lane's 16 dims, quantised: params of its group and the codes, nibble i of w[0] dim i, of w[1] dim 8 + i.
 // SQUARES: adds up the squares.
 template <typename T, int GROUP, bool SQUARES>
-__device__ __forceinline__ GroupParams quantise16(const Raw<T>& raw, const T* rows, uint32_t (&w)[2], float& squares) {
+__device__ __forceinline__ GroupParams quantise16(const Raw<T>& raw, const T* rows, uint32_t sixteen, uint32_t (&w)[2],
+                                                  float& squares) {
   float x[16];
   load8(reinterpret_cast<const T*>(raw.u), *reinterpret_cast<float(*)[8]>(x));
   load8(reinterpret_cast<const T*>(raw.u) + 8, *reinterpret_cast<float(*)[8]>(x + 8));
@@ -180,11 +209,12 @@ __device__ __forceinline__ GroupParams quantise16(const Raw<T>& raw, const T* ro
     codes16(x, g, inv, rows);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      // sum of (0x4B400000 + code) 16^i; what the floats' upper bits add up to is taken off again
-      uint32_t sum = 0u - 0x4B400000u * 0x11111111u;
+      // sum of (0x4B400000 + code) 16^i; what the floats' upper bits add up to is taken off again.  (16 comes in
+      // as a value: as a literal it would be a shift and add at half the rate of multiply-add)
+      uint32_t sum = __float_as_uint(x[8 * j + 7]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = __float_as_uint(x[8 * j + i]) * (1u << (4 * i)) + sum;
-      w[j] = sum;
+      for (int i = 6; i >= 0; --i) sum = sum * sixteen + __float_as_uint(x[8 * j + i]);
+      w[j] = sum - 0x4B400000u * 0x11111111u;
     }
   }
   return g;
@@ -257,6 +287,8 @@ struct WriteArgs {
   uint16_t* tags;           // [n_pages, H, n_rounds, page] or null
   unsigned rows;            // B * H * T
   int n_rounds;
+  bool wide;                // k and v on 32-byte boundaries
+  uint32_t sixteen;         // 16
   Pages pg;
 };
 
@@ -274,9 +306,9 @@ __global__ void __launch_bounds__(kRwThreads, 4) cache_write_kernel(const WriteA
   const long long from = (long long)row * D + j * 16;
   float sq, none;
   const T *k = static_cast<const T*>(a.k) + from, *v = static_cast<const T*>(a.v) + from;
-  const Raw<T> raw_k(k, live), raw_v(v, live);  // of padding nothing is read
-  const GroupParams gk = quantise16<T, GROUP, true>(raw_k, k, wk, sq);
-  const GroupParams gv = quantise16<T, GROUP, false>(raw_v, v, wv, none);
+  const Raw<T> raw_k(k, live, a.wide), raw_v(v, live, a.wide);  // of padding nothing is read
+  const GroupParams gk = quantise16<T, GROUP, true>(raw_k, k, a.sixteen, wk, sq);
+  const GroupParams gv = quantise16<T, GROUP, false>(raw_v, v, a.sixteen, wv, none);
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   k_to_words(wk, j & 1);
@@ -310,25 +342,28 @@ struct ReadArgs {
   void *k, *v;      // [B, H, T, D]
   float* inv;       // [B, H, T] or null
   unsigned rows;
+  bool wide;        // k and v on 32-byte boundaries
   Pages pg;
 };
 
 // z + s code of the 16 codes, rounded once, to 16 consecutive elements.
-__device__ __forceinline__ void store16(float* p, const uint32_t (&w)[2], uint32_t params) {
+__device__ __forceinline__ void store16(float* p, const uint32_t (&w)[2], uint32_t params, bool wide) {
   const float s = bf16_bits(params & 0xffffu), z = __uint_as_float(params & 0xffff0000u);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    float x[8];
+    alignas(16) float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       x[i] = fmaf(s, __uint_as_float(((w[j] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f, z);
-    store8(p + 8 * j, x);
+    const float4* y = reinterpret_cast<const float4*>(x);
+    st32(p + 8 * j, *reinterpret_cast<const uint4*>(y), *reinterpret_cast<const uint4*>(y + 1), wide);
   }
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&w)[2], uint32_t params) {
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&w)[2], uint32_t params, bool wide) {
   const uint32_t s2 = __byte_perm(params, 0, 0x1010), z2 = __byte_perm(params, 0, 0x3232);
   const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2), z = *reinterpret_cast<const __nv_bfloat162*>(&z2);
   const uint32_t c128 = 0x43004300u;  // 0x4300 | code is 128 + code in bf16
+  uint4 u[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     uint32_t y[4];  // dims i and i + 4
@@ -339,13 +374,12 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint32_t (&w)[2]
                                                   *reinterpret_cast<const __nv_bfloat162*>(&c128)), z);
       y[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    uint4 u;
-    u.x = __byte_perm(y[0], y[1], 0x5410);
-    u.y = __byte_perm(y[2], y[3], 0x5410);
-    u.z = __byte_perm(y[0], y[1], 0x7632);
-    u.w = __byte_perm(y[2], y[3], 0x7632);
-    *reinterpret_cast<uint4*>(p + 8 * j) = u;
+    u[j].x = __byte_perm(y[0], y[1], 0x5410);
+    u[j].y = __byte_perm(y[2], y[3], 0x5410);
+    u[j].z = __byte_perm(y[0], y[1], 0x7632);
+    u[j].w = __byte_perm(y[2], y[3], 0x7632);
   }
+  st32(p, u[0], u[1], wide);
 }
 
 template <typename T, int D, int GROUP>
@@ -376,8 +410,8 @@ __global__ void __launch_bounds__(kRwThreads) cache_read_kernel(const ReadArgs a
   words_to_v(wv, lane);
   if (!live) return;
   const long long at = (long long)row * D + j * 16;
-  store16(static_cast<T*>(a.k) + at, wk, pk);
-  store16(static_cast<T*>(a.v) + at, wv, pv);
+  store16(static_cast<T*>(a.k) + at, wk, pk, a.wide);
+  store16(static_cast<T*>(a.v) + at, wv, pv, a.wide);
   if (a.inv && j == 0) a.inv[row] = inv;
 }
 
