@@ -276,8 +276,13 @@ __device__ __forceinline__ Row row_of(const Pages& p, unsigned row) {
   r.b = (int)p.div_h.of(r.bh);
   r.h = (int)(r.bh - (unsigned)r.b * p.H);
   r.pos = row_pos(p, r.b, r.t);
-  r.phys = r.pos >= 0 ? page_of(p, r.b, r.pos >> p.page_log2) : -1;
+  r.phys = -1;
   return r;
+}
+
+// Looks the row's page up (apart from row_of so that a row's own loads need not wait for it).
+__device__ __forceinline__ void look_up_page(const Pages& p, Row& r) {
+  if (r.pos >= 0) r.phys = page_of(p, r.b, r.pos >> p.page_log2);
 }
 
 struct WriteArgs {
@@ -299,21 +304,21 @@ __global__ void __launch_bounds__(kRwThreads, 4) cache_write_kernel(const WriteA
   const unsigned row = blockIdx.x * (kRwThreads / kLanes) + threadIdx.x / kLanes;
   const int j = threadIdx.x % kLanes, lane = threadIdx.x & 31;
   Row r;
-  r.phys = -1;
+  r.pos = r.phys = -1;
   if (row < a.rows) r = row_of(a.pg, row);
-  const bool live = r.phys >= 0;
   uint32_t wk[2], wv[2];
   const long long from = (long long)row * D + j * 16;
   float sq, none;
   const T *k = static_cast<const T*>(a.k) + from, *v = static_cast<const T*>(a.v) + from;
-  const Raw<T> raw_k(k, live, a.wide), raw_v(v, live, a.wide);  // of padding nothing is read
+  const Raw<T> raw_k(k, r.pos >= 0, a.wide), raw_v(v, r.pos >= 0, a.wide);  // of padding nothing is read
+  look_up_page(a.pg, r);
   const GroupParams gk = quantise16<T, GROUP, true>(raw_k, k, a.sixteen, wk, sq);
   const GroupParams gv = quantise16<T, GROUP, false>(raw_v, v, a.sixteen, wv, none);
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   k_to_words(wk, j & 1);
   v_to_words(wv, lane);
-  if (!live) return;
+  if (r.phys < 0) return;
   const int t = r.pos & 15;
   uint8_t* tile = a.cache + tile_offset(a.pg, r.phys, r.h, r.pos, F::kTile);
   const LaneWords<D> at(t, j);
@@ -392,7 +397,8 @@ __global__ void __launch_bounds__(kRwThreads) cache_read_kernel(const ReadArgs a
   uint32_t wk[2] = {0u, 0u}, wv[2] = {0u, 0u}, pk = 0, pv = 0;
   float inv = 0.f;
   if (live) {
-    const Row r = row_of(a.pg, row);
+    Row r = row_of(a.pg, row);
+    look_up_page(a.pg, r);
     if (r.phys >= 0) {
       const int t = r.pos & 15, grp = j / (GROUP / 16);
       const uint8_t* tile = a.cache + tile_offset(a.pg, r.phys, r.h, r.pos, F::kTile);
