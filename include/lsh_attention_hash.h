@@ -406,8 +406,8 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *              (other streams, graphs replayed at the same time) need one each
  *
  * The products with the codes are exact integer sums of fixed-point numbers: a query in steps of
- * its largest entry / 32639 (fp32: / 8355711), a weight in steps of the largest of its 64 keys'
- * weights / 65535 (fp32: / 8388607).  Everything else is fp32; keys in any order give the same
+ * its largest entry / 8355711, a weight in steps of the largest of its 64 keys' weights / 65535
+ * (fp32 queries: / 8388607).  Everything else is fp32; keys in any order give the same
  * result only up to rounding, the same call the same bits.
  * lse makes the result joinable with other key sets by lsh_combine_rounds, where one of
  * them has a key for the row.

@@ -13,9 +13,9 @@
 // their number per code decides.  Both products are mma.m16n8k32 of 8-bit integers: a word's 8
 // codes become bytes by two masks and at most one shift (16 codes as bf16 took 15 instructions,
 // as bytes 6 for K and 8 for V, and one product covers twice the depth).
-//   K: the query is a fixed-point number of the column's largest |q|: 16 bits for bf16 queries,
-//      24 for fp32 ones.  The sums are exact; the rounding of q is 2^-16 (2^-24) of its
-//      largest entry.
+//   K: the query is a fixed-point number of 24 bits of the column's largest |q|.  The sums are
+//      exact; the rounding of q is 2^-24 of its largest entry.  (16 bits would save a product in
+//      three, but their rounding, the same for every key, moves the log-sum-exp by 1e-4.)
 //   V: the weights p_j s_j of a stage's 64 keys are fixed-point numbers of the largest of them,
 //      16 bits for bf16 queries and 23 for fp32 ones; the sums go into float accumulators
 //      after every stage.  A scale for each stage and not for the whole sequence: however many
@@ -24,7 +24,7 @@
 //      the 16 out.  An accumulator that starts at 0x4B400000 is, read as a float, 1.5 * 2^23
 //      plus the sum, so the integers become floats by one subtraction.
 //
-// A number's two bytes are two columns of the product (fp32's third byte a second product), so a
+// A number's two upper bytes are two columns of the product (a third byte is a second product), so a
 // fragment's 8 columns are 4 numbers: CW queries of each of TP = 4 / CW tiles, tile i's
 // products using a B operand that is zero outside its own columns.  A single query thus
 // fills all lanes: lane 4 g + t4 has keys g and g + 8 of tile t4, and scales, exponentials and
@@ -206,9 +206,10 @@ struct AttendCfg {
   using F = Fmt<D, GROUP>;
   static_assert(CW == 4 || NT == 1, "more than 4 queries go in whole fragments");
   static constexpr bool kF32 = sizeof(TQ) == 4;
-  static constexpr int kSets = kF32 ? 2 : 1;  // products for the bytes of a number: (upper, lower) columns; (third, none)
+  // products for the bytes of a weight and of a query: (upper, lower) columns; (third, none)
+  static constexpr int kSets = kF32 ? 2 : 1, kSetsQ = 2;
   // a query's largest number (signed bytes: 127 in each) and a weight's (unsigned)
-  static constexpr int kTop = kF32 ? 127 * 65536 + 127 * 256 + 127 : 127 * 256 + 127;
+  static constexpr int kTop = 127 * 65536 + 127 * 256 + 127;
   static constexpr int kTopW = kF32 ? 0x7fffff : 0xffff;
   static constexpr int kMt = D / 16;       // m tiles of V^T P^T
   static constexpr int kTp = 4 / CW;       // tiles of a fragment
@@ -221,7 +222,7 @@ struct AttendCfg {
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
   static constexpr int kMerge = kAttWarps * kStreams * D * 4;
   static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kOffQs = kOffQ + kSets * NT * kTp * (D / 32) * 32 * 8;
+  static constexpr int kOffQs = kOffQ + kSetsQ * NT * kTp * (D / 32) * 32 * 8;
   static constexpr int kOffMl = kOffQs + (kQ * (F::kGroups + 1) * 4 + 15) / 16 * 16;
   static constexpr int kOffEnt = kOffMl + kAttWarps * kStreams * 8;
   static_assert(kOffEnt % 16 == 0, "16-byte entries");
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kAttThreads, AttendCfg<TQ, D, GROUP, CW, NT>::
 cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   using F = Fmt<D, GROUP>;
-  constexpr int NG = F::kGroups, MT = C::kMt, SETS = C::kSets, TP = C::kTp, ST = C::kSt, SF = C::kSf;
+  constexpr int NG = F::kGroups, MT = C::kMt, SETS = C::kSets, SQ = C::kSetsQ, TP = C::kTp, ST = C::kSt, SF = C::kSf;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int abort_flag;
@@ -435,9 +436,9 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     const bool lower = (l >> 2) & 1;
     const float step = qstep[cc];
     const float inv = step > 0.f ? 1.f / step : 0.f;
-    uint32_t v[SETS][2];
+    uint32_t v[SQ][2];
 #pragma unroll
-    for (int p = 0; p < SETS; ++p) v[p][0] = v[p][1] = 0u;
+    for (int p = 0; p < SQ; ++p) v[p][0] = v[p][1] = 0u;
     if (col < a.cols) {
       const TQ* q = q_row(col) + 32 * w + 2 * (l & 3);
 #pragma unroll
@@ -448,17 +449,15 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           // x / step; a step too small to invert (denormal queries) is divided by
           const float y = inv < INFINITY ? x * inv : x / step;
           int f = max(-C::kTop, min(C::kTop, __float2int_rn(y)));
-          if (C::kF32) {
-            const int b0 = (int8_t)f;  // the third byte
-            if (!lower) v[SETS - 1][e] |= (uint32_t)(b0 & 255) << (8 * j);
-            f = (f - b0) >> 8;
-          }
+          const int b0 = (int8_t)f;  // the third byte
+          if (!lower) v[1][e] |= (uint32_t)(b0 & 255) << (8 * j);
+          f = (f - b0) >> 8;
           const int b1 = (int8_t)f, b2 = (f - b1) >> 8;
           v[0][e] |= (uint32_t)((lower ? b1 : b2) & 255) << (8 * j);
         }
     }
 #pragma unroll
-    for (int p = 0; p < SETS; ++p)
+    for (int p = 0; p < SQ; ++p)
 #pragma unroll
       for (int t = 0; t < TP; ++t)
         reinterpret_cast<uint2*>(qf + (((p * NT + nt) * TP + t) * (D / 64) + (w >> 1)) * 32 + l)[w & 1] =
@@ -524,7 +523,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     float s[SF][NT][2];
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
-      int part[SETS][NT][NG][4];
+      int part[SQ][NT][NG][4];
 #pragma unroll
       for (int i = 0; i < TP; ++i) {
         const uint8_t* tb = buf + (f * TP + i) * F::kTile;  // (a missing tile's sums are replaced below)
@@ -542,7 +541,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
             y[e][3] = (wb[w + e] >> 4) & 0x0f0f0f0fu;
           }
 #pragma unroll
-          for (int p = 0; p < SETS; ++p)
+          for (int p = 0; p < SQ; ++p)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint4 q = qf[(((p * NT + nt) * TP + i) * (D / 64) + w / 2) * 32 + lane];
@@ -573,7 +572,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           for (int nt = 0; nt < NT; ++nt) {
             // at most 64 * 15 * 2^15; the third byte joins in float
             float v = (float)(part[0][nt][n][2 * r] * 256 + part[0][nt][n][2 * r + 1]);
-            if (SETS == 2) v = fmaf(v, 256.f, (float)part[SETS - 1][nt][n][2 * r]);
+            v = fmaf(v, 256.f, (float)part[1][nt][n][2 * r]);
             acc[nt][r] = fmaf(sc, v, acc[nt][r]);
             zero[nt][r] = fmaf(ze, qsum[nt][n], zero[nt][r]);
           }

@@ -215,13 +215,13 @@ def test_write_bad_pages_and_lengths_are_skipped():
 def _bounds(q, K, zK, V, zV, sV, w, key_scale, f32_in, f32_out, want):
     """Bound of the output's error per dim, and of the lse's, from the roundings that the kernel states.
 
-    Logit of key j: the code part sum_d q_d (K - z)_jd takes q rounded to half a step, step = max|q| / 32639
-    (fp32: / 8355711); the integer sums are exact; what float does to the code part and to z's part is
+    Logit of key j: the code part sum_d q_d (K - z)_jd takes q rounded to half a step, step = max|q| /
+    8355711; the integer sums are exact; what float does to the code part and to z's part is
     within 2^-20 of their sizes.  Weights p s go in as fixed-point numbers of the largest of their stage:
     half a step, 1 / 65535 (fp32: 1 / 8388607) of it, times codes of at most 15; the largest of any stage is
     at most the largest of all.  exp2 and the other float steps are within 2^-18 of the sizes.
     """
-    step = np.abs(q).max() / (8355711 if f32_in else 32639)
+    step = np.abs(q).max() / 8355711
     code = np.abs(K - zK)
     dz = ((0.5 * step * code.sum(1) + 2.0 ** -20 * ((code + np.abs(zK)) @ np.abs(q))) * key_scale).max() + 2.0 ** -20
     unit = (w[:, None] * sV).max(0) / (8388607 if f32_in else 65535)
