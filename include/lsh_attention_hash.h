@@ -310,7 +310,7 @@ LSH_API lsh_status lsh_chunk_attend_backward(const void* qk, const void* v, int 
  * call's among them.  Of the T rows of a call the first new_len[b] belong to sequence b
  * (new_len null: all T) and are its last tokens: row i is position ctx_len[b] -
  * new_len[b] + i.  Rows at or behind new_len[b], and rows whose position would be
- * negative, are padding.  All three arrays are read on the device, so a captured graph
+ * negative, are padding (a new_len above T counts as T).  All three arrays are read on the device, so a captured graph
  * replays with their current contents.
  *
  * Caller errors that only the device can see are recorded as LSH_ERR_INVALID_ARG in the
@@ -407,7 +407,8 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *
  * The products with the codes are exact integer sums of fixed-point numbers: a query in steps of
  * its largest entry / 8355711, a weight in steps of the largest of its 64 keys' weights / 65535
- * (fp32 queries: / 8388607).  Everything else is fp32; keys in any order give the same
+ * (fp32 queries: / 8388607).  A query row with an infinity or a NaN answers NaN; stored values may
+ * reach 1e36 (beyond that a weight times a scale can overflow).  Everything else is fp32; keys in any order give the same
  * result only up to rounding, the same call the same bits.
  * lse makes the result joinable with other key sets by lsh_combine_rounds, where one of
  * them has a key for the row.

@@ -316,15 +316,25 @@ def _fit(t, name, dtype, shape, dev):
     raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
-def _on_device(dev, stream, fn, where, *args):
-    """Calls ``fn(*args, stream pointer)`` with ``dev`` current (decoding steps are short: no more host work
-    than it takes)."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    else:
-        if stream.device != dev:
-            raise ValueError(f"{where}: the stream must be on {dev}")
-        raw = stream.cuda_stream
+def _on_stream(fn):
+    """``stream=s`` runs the whole call with ``s`` current, so that what it allocates belongs to ``s`` too."""
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw, device=stream.device)
+
+    return call
+
+
+def _on_device(dev, device, fn, where, *args):
+    """Calls ``fn(*args, current stream of dev)`` with ``dev`` current (decoding steps are short: no more host
+    work than it takes).  ``device``: the given stream's, or None."""
+    if device is not None and device != dev:
+        raise ValueError(f"{where}: the tensors are on {dev}, the stream on {device}")
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch._C._cuda_getDevice() == dev.index:
         code = fn(*args, raw)
     else:
@@ -396,8 +406,9 @@ def _rows4(t, name):
     return t.shape
 
 
+@_on_stream
 def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_len=None, buckets=None, tags=None,
-                    stream=None):
+                    device=None):
     """Quantises rows ``k``, ``v`` [B,H,T,D] into the 4-bit ``cache`` at their positions.
 
     ``ctx_len`` [B] int32 counts each sequence's cached tokens, these rows among them; the first
@@ -421,13 +432,14 @@ def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_
         n_rounds = _rows4(tags, "tags")[2]
         tg = _fit(tags, "tags", torch.int16, (n_pages, H, n_rounds, page), dev)
         bk = _fit(buckets, "buckets", torch.int32, (B, H, n_rounds, T), dev)
-    _on_device(dev, stream, lib.lsh_cache_write, "lsh_cache_write", k.data_ptr(), _fit(v, "v", k.dtype, shape, dev), dt,
+    _on_device(dev, device, lib.lsh_cache_write, "lsh_cache_write", k.data_ptr(), _fit(v, "v", k.dtype, shape, dev), dt,
                B, H, T, D, bk, n_rounds, ctx, new, table, max_pages, page, group,
                _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, tg)
 
 
+@_on_stream
 def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_len=None, out_dtype=torch.bfloat16,
-                   k=None, v=None, key_inv=None, stream=None):
+                   k=None, v=None, key_inv=None, device=None):
     """The stored values of each sequence's last ``new_len[b]`` (default T) tokens.
 
     Returns (k, v [B,H,T,D] ``out_dtype``, key_inv [B,H,T] float32: 1 / length of the K rows as
@@ -443,13 +455,14 @@ def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_l
     k, kp = _new(k, "k", out_dtype, shape, cache)
     v, vp = _new(v, "v", out_dtype, shape, k)
     key_inv, ip = _new(key_inv, "key_inv", torch.float32, shape[:3], cache)
-    _on_device(dev, stream, lib.lsh_cache_read, "lsh_cache_read", cache.data_ptr(), n_pages, B, H, T, D, ctx, new, table,
+    _on_device(dev, device, lib.lsh_cache_read, "lsh_cache_read", cache.data_ptr(), n_pages, B, H, T, D, ctx, new, table,
                max_pages, page, group, kp, vp, _DT[out_dtype], ip)
     return k, v, key_inv
 
 
+@_on_stream
 def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=None, n_local=1, causal=True,
-                     selected=None, scores=None, stream=None):
+                     selected=None, scores=None, device=None):
     """The ``n_select`` pages that each new token attends to: (selected, scores).
 
     ``q_buckets`` [B,Hq,n_rounds,T] int32 are the new rows' buckets.  ``scores`` [B,H,T,max_pages]
@@ -468,7 +481,7 @@ def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=
         raise ValueError("n_select must be at least 1")
     selected, sp = _new(selected, "selected", torch.int32, (B, H, T, n_select), tags)
     scores, cp = _new(scores, "scores", torch.int32, (B, H, T, max_pages), tags)
-    _on_device(dev, stream, lib.lsh_cache_select, "lsh_cache_select",
+    _on_device(dev, device, lib.lsh_cache_select, "lsh_cache_select",
                _fit(tags, "tags", torch.int16, tags.shape, dev), n_pages,
                _fit(q_buckets, "q_buckets", torch.int32, q_buckets.shape, dev), B, Hq, H, T, n_rounds, ctx, new, table,
                max_pages, page, n_select, n_local, 2 if causal else 0, sp, cp)
@@ -486,9 +499,10 @@ def lsh_cache_attend_workspace_bytes(dtype, B, Hq, H, T, D, max_pages, page, n_s
     return int(load_library().lsh_cache_attend_workspace_bytes(_DT[dtype], B, Hq, H, T, D, max_pages, page, n_select))
 
 
+@_on_stream
 def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_len=None, selected=None,
                      self_mask=True, causal=True, unit_keys=True, scale=None, out_dtype=None, out=None, lse=None,
-                     workspace=None, stream=None):
+                     workspace=None, device=None):
     """Attention of the new rows' queries ``q`` [B,Hq,T,D] over their sequences' cached tokens.
 
     Returns (out [B,Hq,T,D], lse [B,Hq,T] float32).  Hq is a multiple of the cache's H.
@@ -521,7 +535,7 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
             ws = workspace.data_ptr()
     else:
         ws, nbytes = _fit(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
-    _on_device(dev, stream, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D,
+    _on_device(dev, device, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D,
                _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, ctx, new, table, max_pages, page, group, sel,
                n_select, (1 if self_mask else 0) | (2 if causal else 0), 1 if unit_keys else 0,
                0.0 if scale is None else float(scale), op, _DT[out_dtype], lp, ws, nbytes)
@@ -579,25 +593,29 @@ def lsh_attention_decode(qk, v, R, n_buckets, cache, tags, page_table, ctx_len, 
     b = bufs or {}
     if n_select and tags is None:
         raise ValueError("n_select needs tags")
-    if isinstance(qk, torch.Tensor) and qk.is_cuda and torch.cuda.current_device() != qk.device.index:
-        with torch.cuda.device(qk.device):
+    dev = _need(qk, "qk").device
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"lsh_attention_decode: the tensors are on {dev}, the stream on {stream.device}")
+        # what the step allocates in between belongs to the stream it runs on
+        with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
             return lsh_attention_decode(qk, v, R, n_buckets, cache, tags, page_table, ctx_len, page=page, group=group,
                                         new_len=new_len, n_select=n_select, n_local=n_local, self_mask=self_mask,
-                                        scale=scale, stream=stream, bufs=bufs, check=check)
+                                        scale=scale, bufs=bufs, check=check)
     buckets = None
     if tags is not None:
-        buckets, _ = lsh_hash(qk, R, n_buckets, buckets=b.get("buckets"), with_near_tie=False, stream=stream)
+        buckets, _ = lsh_hash(qk, R, n_buckets, buckets=b.get("buckets"), with_near_tie=False)
     lsh_cache_write(qk, v, cache, page_table, ctx_len, page=page, group=group, new_len=new_len, buckets=buckets,
-                    tags=tags, stream=stream)
+                    tags=tags)
     selected = None
     if n_select:
         selected, _ = lsh_cache_select(tags, buckets, page_table, ctx_len, n_select, new_len=new_len, n_local=n_local,
-                                       selected=b.get("selected"), scores=b.get("scores"), stream=stream)
+                                       selected=b.get("selected"), scores=b.get("scores"))
     out, lse = lsh_cache_attend(qk, cache, page_table, ctx_len, page=page, group=group, new_len=new_len,
                                 selected=selected, self_mask=self_mask, scale=scale, out=b.get("out"),
-                                lse=b.get("lse"), workspace=b.get("workspace"), stream=stream)
+                                lse=b.get("lse"), workspace=b.get("workspace"))
     if check:
-        _check(lsh_get_device_status(stream), "lsh_attention_decode (device status)")
+        _check(lsh_get_device_status(), "lsh_attention_decode (device status)")
     return out, lse
 
 

@@ -71,11 +71,13 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
   const bool sel = n_select > 0;
   p.units = (long long)B * H * (sel ? T : 1);
   p.cols = sel ? G : G * T;
-  // one or two columns: four or two tiles share a fragment; beyond four, fragments side by side (a
-  // cached token is unpacked once for up to 16 columns; at D 256, and in fp32, registers hold 8)
-  const int most = dtype == LSH_F32 || D == 256 ? 2 : 4;
+  // one or two columns: four or two tiles share a fragment; beyond four, fragments side by side, so
+  // that a cached token is unpacked once for up to 16 columns (8 heads of 64K, D 128: 16 queries take
+  // 275 us that way and four times 113 us by fours).  fp32 and D 256 have registers for two
+  // fragments, fp32 at D 256 for one (the second would spill 1.9 KB a thread).
+  const int most = D == 256 ? (dtype == LSH_F32 ? 1 : 2) : (dtype == LSH_F32 ? 2 : 4);
   p.cw = p.cols >= 3 ? 4 : p.cols == 2 ? 2 : 1;
-  p.nt = p.cols <= 4 ? 1 : p.cols <= 8 ? 2 : most;
+  p.nt = p.cols <= 4 ? 1 : p.cols <= 8 ? std::min(2, most) : most;
   p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
   const long long keys = (long long)(sel ? n_select : max_pages) * page;
   p.direct = keys <= 1024;
@@ -339,12 +341,13 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
     if (p.cw == 1) return launch_cache_attend<TQ, DD, GG, 1, 1>(a, p, s);       \
     if (p.cw == 2) return launch_cache_attend<TQ, DD, GG, 2, 1>(a, p, s);       \
     if (p.nt == 1) return launch_cache_attend<TQ, DD, GG, 4, 1>(a, p, s);       \
-    if (p.nt == 2) return launch_cache_attend<TQ, DD, GG, 4, 2>(a, p, s);       \
   } while (0)
     if (dtype == LSH_F32) {
       LSH_CA(float);
+      if constexpr (DD <= 128) return launch_cache_attend<float, DD, GG, 4, 2>(a, p, s);
     } else {
       LSH_CA(bf);
+      if (p.nt == 2) return launch_cache_attend<bf, DD, GG, 4, 2>(a, p, s);
       if constexpr (DD <= 128) return launch_cache_attend<bf, DD, GG, 4, 4>(a, p, s);
     }
 #undef LSH_CA

@@ -673,8 +673,9 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         const float wm = __uint_as_float(t);
         unit[nt][n] = wm * (1.f / C::kTopW);
         // weights below 2^-110 are nothing (a value's scale is 2^-100 at least); NaN and infinity stay
-        // in the unit
-        const float inv = wm > 7.7037197775489434e-34f ? __fdividef((float)C::kTopW, wm) : 0.f;
+        // in the unit; both sides 2^-16 smaller, as the quick division's divisor ends at 2^126
+        constexpr float k16 = 1.f / 65536.f;
+        const float inv = wm > 7.7037197775489434e-34f ? __fdividef((float)C::kTopW * k16, wm * k16) : 0.f;
 #pragma unroll
         for (int f = 0; f < SF; ++f) {
           uint32_t x[2];  // the number in the low bits of a float's mantissa

@@ -631,3 +631,127 @@ def test_joins_with_exact_recent_rows():
     out, lse = lsh.lsh_combine_rounds(o, l)
     whole, wl = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, out_dtype=torch.float32, **c.form)
     assert torch.allclose(lse, wl, atol=1e-4) and (out - whole).abs().max() < 2.0 ** -7
+
+
+# ---------------------------------------------------------------------------------------------------
+# Sizes and layouts beyond the ordinary
+
+def test_write_on_16_byte_boundaries():
+    """Rows and outputs that start on a 16-byte but not on a 32-byte boundary give the same bytes."""
+    c = Cache(70, B=1, H=2, ctx=(75,))
+    n = c.k.numel()
+    for dt in (torch.bfloat16, torch.float32):
+        off = 16 // torch.empty(0, dtype=dt).element_size()
+        big = torch.empty(2, n + 2 * off, dtype=dt, device=DEV)
+        k, v = (big[i, off:off + n].view(c.k.shape) for i in range(2))
+        k.copy_(c.k)
+        v.copy_(c.v)
+        assert (k.data_ptr() | v.data_ptr()) % 32 == 16 or dt == torch.float32
+        other = torch.full_like(c.cache, 0xFF)
+        lsh.lsh_cache_write(k, v, other, c.table, c.ctx_len, **c.form)
+        assert torch.equal(other, c.cache)
+        lsh.lsh_cache_read(c.cache, c.table, c.ctx_len, 75, 128, out_dtype=dt, k=k, v=v, **c.form)
+        kk, vv, _ = lsh.lsh_cache_read(c.cache, c.table, c.ctx_len, 75, 128, out_dtype=dt, **c.form)
+        assert torch.equal(k, kk) and torch.equal(v, vv)
+
+
+@pytest.mark.parametrize("B", [33, 70])
+def test_many_sequences(B):
+    """More sequences than a warp scans at a time, many of them empty, all lengths."""
+    g = torch.Generator().manual_seed(B)
+    ctx = [int(x) for x in torch.randint(0, 400, (B,), generator=g)]
+    ctx[0], ctx[5], ctx[31], ctx[32] = 0, 2000, 0, 1
+    c = Cache(71, B=B, H=1, D=64, page=16, ctx=ctx)
+    q = c.rand(B, 2, 1, 64).to(DEV)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, **c.form)
+    _check_attend(c, q, out, lse, [1] * B)
+    sel = torch.randint(0, 125, (B, 1, 1, 70), generator=g, dtype=torch.int32)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, selected=sel.to(DEV), **c.form)
+    _check_attend(c, q, out, lse, [1] * B, selected=sel)
+
+
+def test_long_pieces_of_small_pages():
+    """A CTA's stretch of the keys longer than the pages it looks up at a time (256 of 16 tokens)."""
+    n, H, D = 500000, 8, 64
+    g = torch.Generator(device=DEV).manual_seed(72)
+    k = torch.randn(1, H, n, D, generator=g, device=DEV).bfloat16()
+    v = torch.randn(1, H, n, D, generator=g, device=DEV).bfloat16()
+    q = torch.randn(1, H, 1, D, generator=g, device=DEV).bfloat16()
+    ctx = torch.tensor([n], dtype=torch.int32, device=DEV)
+    got = []
+    for page in (16, 256):
+        pages = -(-n // page)
+        cache, _ = lsh.alloc_cache(pages, H, D, page=page, device=DEV)
+        table = torch.randperm(pages, generator=g, device=DEV).int()[None]
+        lsh.lsh_cache_write(k, v, cache, table, ctx, page=page)
+        got.append(lsh.lsh_cache_attend(q, cache, table, ctx, page=page, out_dtype=torch.float32))
+        K, V, inv = lsh.lsh_cache_read(cache, table, ctx, n, D, page=page, out_dtype=torch.float32)
+    K, V, inv = (t[0, :, :-1].double() for t in (K, V, inv))
+    z = torch.einsum("hnd,hd->hn", K, q[0, :, 0].double()) * inv / 8
+    want = torch.einsum("hn,hnd->hd", torch.softmax(z, 1), V)
+    for out, lse in got:
+        # weights in 1/65535 of their stage's largest, codes to 15, scales to 0.5; over 500000 keys
+        # their roundings, half a step each and independent, add up to far less than the 2^-12 asked for
+        assert (out[0, :, 0].double() - want).abs().max() < 2.0 ** -12
+        assert (lse[0, :, 0].double() - torch.logsumexp(z, 1)).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("v_size", [1e-25, 1e25, 1e35])
+def test_attend_value_range(v_size):
+    """Values far from 1 in size; some rows far larger than the others, at keys that hardly count."""
+    g = torch.Generator().manual_seed(73)
+    k, v = torch.randn(1, 1, 300, 64, generator=g), torch.randn(1, 1, 300, 64, generator=g) * v_size
+    v[:, :, ::7] *= 1e-6
+    c = Cache(74, B=1, H=1, D=64, dtype=torch.float32, ctx=(300,), rows=(k, v))
+    for dt in (torch.float32, torch.bfloat16):
+        q = torch.randn(1, 1, 1, 64, generator=g).to(dt).to(DEV)
+        out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, out_dtype=torch.float32, **c.form)
+        _check_attend(c, q, out, lse, [1])
+
+
+def test_steps_on_another_stream_keep_their_buffers():
+    """What a call on a given stream allocates is not handed out again while that stream still uses it."""
+    c = Cache(75, B=2, H=4, ctx=(6000, 3000))
+    q = c.rand(2, 4, 1, 128).to(DEV)
+    want, _ = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, **c.form)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(30):
+        outs.append(lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, stream=s, **c.form)[0])
+        torch.empty(1 << 20, dtype=torch.uint8, device=DEV).fill_(0xFF)  # would reuse a workspace freed too early
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_binding_checks_on_the_device():
+    c = Cache(76, B=1, H=2, ctx=(40,))
+    q = c.rand(1, 2, 1, 128).to(DEV)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, page=32)           # another form's block
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len.long(), **c.form)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len.cpu(), **c.form)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_attend(q.transpose(1, 3), c.cache, c.table, c.ctx_len, **c.form)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_attend(q.half(), c.cache, c.table, c.ctx_len, **c.form)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_attend(q, c.cache, c.table.repeat(2, 1), c.ctx_len, **c.form)
+    with pytest.raises(lsh.LSHError):
+        lsh.lsh_cache_attend(c.rand(1, 3, 1, 128).to(DEV), c.cache, c.table, c.ctx_len, **c.form)  # 3 heads over 2
+    with pytest.raises(lsh.LSHError):
+        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, group=128, page=64)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_write(q, q[:, :1].contiguous(), c.cache, c.table, c.ctx_len, **c.form)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_select(c.cache, c.table, c.table, c.ctx_len, 1)
+    many = torch.zeros(3, 2, 1, 128, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        lsh.lsh_cache_write(many, many, c.cache, c.table, c.ctx_len, **c.form)
+    table = torch.zeros(1, 40, dtype=torch.int32, device=DEV)  # more than 1024 keys: a workspace
+    with pytest.raises(lsh.LSHError):
+        lsh.lsh_cache_attend(q, c.cache, table, c.ctx_len, workspace=torch.empty(16, dtype=torch.uint8, device=DEV),
+                             **c.form)
+    assert _status() == 0
