@@ -106,6 +106,24 @@ inline lsh_status allow_smem(const void* fn, int bytes, std::atomic<uint64_t>& d
   return LSH_OK;
 }
 
+// Launches a kernel that may be set up before the one ahead of it on the stream has ended: it executes
+// griddepcontrol.wait before it reads or writes anything that others do.
+template <typename Args>
+lsh_status launch_early(void (*fn)(Args), unsigned grid, int threads, int smem, cudaStream_t s,
+                        const std::remove_const_t<Args>& args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+}
+
 template <typename TQ, int D, int GROUP, int CW, int NT>
 lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, cudaStream_t s) {
   using namespace lsh::cache;
@@ -118,20 +136,10 @@ lsh_status launch_cache_attend(lsh::cache::AttendArgs& a, const AttendPlan& p, c
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
   a.direct = p.direct;
   a.nc = p.direct ? (int)(p.units * p.n_ct) : std::min(p.max_ctas, sms * C::kCtas);
-  kfn<<<a.nc, kAttThreads, C::kSmem, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
-  if (p.direct) return LSH_OK;
-  // the join may be set up while the last CTAs run; it waits for them before it reads
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.units * p.cols));
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, a) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+  const lsh_status run = launch_early(kfn, (unsigned)a.nc, kAttThreads, C::kSmem, s, a);
+  if (run != LSH_OK || p.direct) return run;
+  // set up while the last CTAs run; it waits for them before it reads
+  return launch_early(cache_join_kernel<D>, (unsigned)(p.units * p.cols), kJoinThreads, 0, s, a);
 }
 
 }  // namespace
@@ -254,7 +262,7 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
   // SELECT_TWO us as two kernels, SELECT_ONE us as one)
   const bool fused = (long long)max_pages * page * n_rounds * 2 <= 64 * 1024;
   if (!fused && max_pages > 0) {
-    // pages a warp: eight, fewer where that would leave the device with less than 16 warps an SM
+    // pages a warp: 16, fewer where that would leave the device with less than 16 warps an SM
     const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
     int wp = lsh::cache::kWarpPages;
     while (wp > 1 && (long long)B * H * max_pages / wp < 16ll * sms) wp /= 2;
@@ -269,14 +277,13 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
     else if (chunks == 4) lsh::cache::cache_score_kernel<4><<<grid, threads, 0, s>>>(a, groups);
     else lsh::cache::cache_score_kernel<0><<<grid, threads, 0, s>>>(a, groups);
   }
-  const int smem = fused || max_pages > n_select ? std::max(16, max_pages * 4) : 16;
+  const int smem = fused || max_pages > n_select ? std::max(16, (max_pages + 3) / 4 * 16) : 16;
   a.fused = fused;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(lsh::cache::cache_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess)
     return LSH_ERR_CUDA;
-  lsh::cache::cache_pick_kernel<<<(unsigned)rows, lsh::cache::kPickThreads, smem, s>>>(a);
-  return launch_status();
+  return launch_early(lsh::cache::cache_pick_kernel, (unsigned)rows, lsh::cache::kPickThreads, smem, s, a);
 }
 
 size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, int D, int max_pages, int page,

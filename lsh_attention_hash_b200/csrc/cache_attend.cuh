@@ -264,6 +264,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   tc::fence_mbar_init();
   int slot = 0;
   uint32_t phase = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what ran before is done: lengths, pages, rows, workspace
 
   // ---- the CTA's stretch of the work -----------------------------------------------------------------
   long long before = 0, x = 0, x_end = 1;
@@ -831,7 +832,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 
 // Joins the pieces of a column: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, and answers the
 // rows that no item has (padding).
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 512;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_constant__ AttendArgs a) {
@@ -863,6 +864,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c0 == c1) return;  // written by its CTA
   {
+#pragma unroll 4
     for (int c = c0 + part; c <= c1; c += kParts) {
       const long long pi = ((long long)c * 2 + (c == c0 ? 1 : 0)) * a.tile_cols + cc;
       const float2 v = *reinterpret_cast<const float2*>(a.part_ml + 2 * pi);
@@ -882,11 +884,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const __grid_c
   __syncthreads();
   if (part) return;
   float M = -INFINITY;
-#pragma unroll
+#pragma unroll 8
   for (int i = 0; i < kParts; ++i) M = fmaxf(M, sml[i].x);
   sum = 0.f;
   float r[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 8
   for (int i = 0; i < kParts; ++i) {
     const float f = sml[i].x == M ? 1.f : exp2f(sml[i].x - M);
     sum = fmaf(sml[i].y, f, sum);

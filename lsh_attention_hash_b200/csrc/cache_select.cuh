@@ -6,7 +6,7 @@
 // over the page's admissible positions of [tag == bucket of the query].  Whole
 // numbers, so the choice is the same however the sum is split.
 //
-// Scoring reads 2 bytes per token and round and is bound by that: a warp takes eight
+// Scoring reads 2 bytes per token and round and is bound by that: a warp takes up to 16
 // pages of a head, all 16-byte loads of a page (and of the next ones) in flight, and compares two
 // tags an instruction: min(tag ^ bucket, 1) counts those that differ.  The choice is one CTA per
 // query row over its scores in shared memory: a binary search for the lowest score that gets
@@ -20,8 +20,8 @@ namespace lsh {
 namespace cache {
 
 constexpr int kScoreThreads = 256;
-constexpr int kWarpPages = 8;  // most pages of a warp
-constexpr int kPickThreads = 512;
+constexpr int kWarpPages = 16;  // most pages of a warp (at most 32: a lane each)
+constexpr int kPickThreads = 1024;
 constexpr int kMaxPickPages = 49152;  // scores of one row in shared memory (192 KB)
 
 struct SelectArgs {
@@ -78,6 +78,7 @@ __device__ __forceinline__ int page_score(const SelectArgs& a, const int32_t* qb
 // query head, so that the lane's buckets stay in registers; 0: any number.
 template <int NC>
 __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectArgs a, int groups) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the choice may be set up; it waits below
   const int lane = threadIdx.x & 31;
   const Pages& pg = a.pg;
   const unsigned w = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);  // (head, its pages)
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
         q2[k] = q * 0x10001u;
       }
       if (!__any_sync(0xffffffffu, bad)) {
-#pragma unroll 4
+#pragma unroll(NC == 1 ? 8 : 4)
         for (; i < whole; ++i) {
           const int ph = __shfl_sync(0xffffffffu, phys, i);
           uint32_t acc = 0;
@@ -138,32 +139,14 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
   }
 }
 
-// Maximum and sum over the block; every thread gets them.
-__device__ __forceinline__ int block_max(int v, int* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int m = red[0];
-  for (int i = 1; i < kPickThreads / 32; ++i) m = max(m, red[i]);
-  __syncthreads();
-  return m;
-}
-
-__device__ __forceinline__ int block_count(int v, int* red) {
-  v = __reduce_add_sync(0xffffffffu, v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int m = 0;
-  for (int i = 0; i < kPickThreads / 32; ++i) m += red[i];
-  __syncthreads();
-  return m;
-}
-
 __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectArgs a) {
-  extern __shared__ int sc[];
-  __shared__ int red[kPickThreads / 32];
+  extern __shared__ __align__(16) int sc[];
+  __shared__ int cell[4];  // the largest score; counts of three steps in turn
   __shared__ int2 scan[kPickThreads / 32];
   const Pages& pg = a.pg;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what follows waits for this kernel's end
+  asm volatile("griddepcontrol.wait;" ::: "memory");               // the scores are there
+  if (threadIdx.x < 4) cell[threadIdx.x] = 0;
   const long long row = blockIdx.x;
   const int t = (int)(row % pg.T);
   const int b = (int)(row / pg.T / pg.H);
@@ -189,22 +172,57 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectAr
   }
   const int n_free = n - a.n_local;          // pages that the score decides about
   const int want = a.n_select - a.n_local;   // of which so many get in (want < n_free)
+  // scores to shared memory, four at a time, with -1 behind the last (max_pages is padded there)
   int best = 0;
-  if (a.fused) __syncthreads();
-  for (int i = threadIdx.x; i < n_free; i += kPickThreads) {
-    const int s = a.fused ? sc[i] : a.scores[row * pg.max_pages + i];
-    sc[i] = s;
-    best = max(best, s);
+  const int n4 = (n_free + 3) / 4;
+  if (a.fused) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < n_free; i += kPickThreads) best = max(best, sc[i]);
+    __syncthreads();
+    for (int i = n_free + threadIdx.x; i < 4 * n4; i += kPickThreads) sc[i] = -1;
+  } else {
+    const int* from = a.scores + row * pg.max_pages;
+    if ((pg.max_pages & 3) == 0) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n4; i += kPickThreads) {
+        int4 u = *reinterpret_cast<const int4*>(from + 4 * i);
+        if (4 * i + 1 >= n_free) u.y = -1;
+        if (4 * i + 2 >= n_free) u.z = -1;
+        if (4 * i + 3 >= n_free) u.w = -1;
+        reinterpret_cast<int4*>(sc)[i] = u;
+        best = max(best, max(max(u.x, u.y), max(u.z, u.w)));
+      }
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < 4 * n4; i += kPickThreads) {
+        const int v = i < n_free ? from[i] : -1;
+        sc[i] = v;
+        best = max(best, v);
+      }
+    }
   }
   for (int i = threadIdx.x; i < a.n_local; i += kPickThreads) out[want + i] = n_free + i;
-  best = block_max(best, red);  // (its barriers also publish sc)
+  if (!a.fused) __syncthreads();  // cell is cleared
+  best = __reduce_max_sync(0xffffffffu, best);
+  if ((threadIdx.x & 31) == 0) atomicMax(cell, best);
+  __syncthreads();  // (and sc is there)
+  best = cell[0];
   // the largest v with at least `want` scores >= v
-  int lo = 0, hi = best + 1;
+  int lo = 0, hi = best + 1, step = 0;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     int cnt = 0;
-    for (int i = threadIdx.x; i < n_free; i += kPickThreads) cnt += sc[i] >= mid;
-    if (block_count(cnt, red) >= want) lo = mid; else hi = mid;
+    for (int i = threadIdx.x; i < n4; i += kPickThreads) {
+      const int4 u = reinterpret_cast<const int4*>(sc)[i];
+      cnt += (u.x >= mid) + (u.y >= mid) + (u.z >= mid) + (u.w >= mid);
+    }
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if ((threadIdx.x & 31) == 0) atomicAdd(cell + 1 + step, cnt);
+    const int next = step == 2 ? 0 : step + 1;
+    if (threadIdx.x == 0) cell[1 + next] = 0;  // (last read two barriers ago)
+    __syncthreads();
+    if (cell[1 + step] >= want) lo = mid; else hi = mid;
+    step = next;
   }
   // a thread's stretch of pages: how many score above lo, how many equal it
   const int per = ((n_free + kPickThreads - 1) / kPickThreads) | 1;  // odd: no shared-memory bank conflicts
