@@ -108,25 +108,31 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
         bad |= q > 65535u;
         q2[k] = q * 0x10001u;
       }
-      if (!__any_sync(0xffffffffu, bad)) {
-#pragma unroll(NC == 1 ? 8 : 4)
-        for (; i < whole; ++i) {
-          const int ph = __shfl_sync(0xffffffffu, phys, i);
-          uint32_t acc = 0;
-          if (ph >= 0) {
+      if (pg.n_pages > 0 && !__any_sync(0xffffffffu, bad)) {
+        constexpr int kBatch = NC == 1 ? 8 : NC == 2 ? 4 : 2;  // pages whose loads are in flight together
+        for (; i < whole; i += kBatch) {
+          uint4 u[kBatch][NC > 0 ? NC : 1];
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) {
+            // (a page that is missing, or behind the last whole one, reads page 0 for nothing)
+            const int ph = max(__shfl_sync(0xffffffffu, phys, min(i + p, 31)), 0);
             const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(a.tags) +
                                                               ((long long)ph * pg.H + h) * row_bytes) + lane;
-            uint4 u[NC > 0 ? NC : 1];
 #pragma unroll
-            for (int k = 0; k < NC; ++k) u[k] = __ldg(src + 32 * k);
-            acc = NC * 0x00040004u;
+            for (int k = 0; k < NC; ++k) u[p][k] = __ldg(src + 32 * k);
+          }
+#pragma unroll
+          for (int p = 0; p < kBatch; ++p) {
+            uint32_t acc = NC * 0x00040004u;
 #pragma unroll
             for (int k = 0; k < NC; ++k)
-              acc -= differ2(u[k].x, q2[k]) + differ2(u[k].y, q2[k]) + differ2(u[k].z, q2[k]) + differ2(u[k].w, q2[k]);
+              acc -= differ2(u[p][k].x, q2[k]) + differ2(u[p][k].y, q2[k]) + differ2(u[p][k].z, q2[k]) +
+                     differ2(u[p][k].w, q2[k]);
+            const int sum = __reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
+            if (lane == i + p && i + p < whole) score = phys >= 0 ? sum : 0;
           }
-          const int sum = __reduce_add_sync(0xffffffffu, (acc & 0xffffu) + (acc >> 16));
-          if (lane == i) score = sum;
         }
+        i = whole;
       }
     }
     // the page that the limit cuts, other sizes, several query heads
@@ -142,6 +148,7 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
 __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) int sc[];
   __shared__ int cell[4];  // the largest score; counts of three steps in turn
+  static_assert(kPickThreads == 1024, "a lane for every warp in the second scan");
   __shared__ int2 scan[kPickThreads / 32];
   const Pages& pg = a.pg;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what follows waits for this kernel's end
@@ -243,13 +250,19 @@ __global__ void __launch_bounds__(kPickThreads) cache_pick_kernel(const SelectAr
   }
   if (lane == 31) scan[warp] = make_int2(pa, pe);
   __syncthreads();
-  int total_above = 0, ba = pa - above, be = pe - equal;
-  for (int i = 0; i < kPickThreads / 32; ++i) {
-    if (i < warp) {
-      ba += scan[i].x;
-      be += scan[i].y;
+  int2 w = scan[lane];  // (kPickThreads / 32 warps: a lane each)
+  for (int o = 1; o < 32; o <<= 1) {
+    const int xa = __shfl_up_sync(0xffffffffu, w.x, o), xe = __shfl_up_sync(0xffffffffu, w.y, o);
+    if (lane >= o) {
+      w.x += xa;
+      w.y += xe;
     }
-    total_above += scan[i].x;
+  }
+  const int total_above = __shfl_sync(0xffffffffu, w.x, 31);
+  int ba = pa - above, be = pe - equal;
+  if (warp > 0) {
+    ba += __shfl_sync(0xffffffffu, w.x, warp - 1);
+    be += __shfl_sync(0xffffffffu, w.y, warp - 1);
   }
   const int need = want - total_above;  // of the equal ones, the first so many
   for (int i = i0; i < i1; ++i) {
