@@ -73,7 +73,7 @@ inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int 
   p.cols = sel ? G : G * T;
   // one or two columns: four or two tiles share a fragment; beyond four, fragments side by side, so
   // that a cached token is unpacked once for up to 16 columns (8 heads of 64K, D 128: 16 queries take
-  // 275 us that way and four times 113 us by fours).  fp32 and D 256 have registers for two
+  // 264 us that way and four times 110 us by fours).  fp32 and D 256 have registers for two
   // fragments, fp32 at D 256 for one (the second would spill 1.9 KB a thread).
   const int most = D == 256 ? (dtype == LSH_F32 ? 1 : 2) : (dtype == LSH_F32 ? 2 : 4);
   p.cw = p.cols >= 3 ? 4 : p.cols == 2 ? 2 : 1;

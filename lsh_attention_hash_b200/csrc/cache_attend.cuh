@@ -46,7 +46,7 @@
 // either way, but a launch and a workspace less: 21 us a call with two kernels, 16 us with one).
 //
 // Measured, one new token, bf16: 8 x 8 heads x 65536 keys of 128 (621 MB) 105 us, 5.9 TB/s, 90 % of the
-// measured copy rate; 8 heads x 1 M keys of 64 (638 MB) 113 us, 5.6 TB/s, 86 %.  Four queries a cached head 113 us, 16 queries 275 us: there
+// measured copy rate; 8 heads x 1 M keys of 64 (638 MB) 113 us, 5.6 TB/s, 86 %.  Four queries a cached head 110 us, 16 queries 264 us: there
 // the integer products and the unpacking (150 instructions a tile for one query) bind.
 // The ring is two stages of 64 tokens a warp and 8 warps an SM at D 128: one stage and 16 warps took as long
 // there and 11 % more at D 64; three stages leave one CTA an SM (42 % more).
@@ -212,8 +212,9 @@ struct AttendCfg {
   using F = Fmt<D, GROUP>;
   static_assert(CW == 4 || NT == 1, "more than 4 queries go in whole fragments");
   static constexpr bool kF32 = sizeof(TQ) == 4;
-  // products for the bytes of a weight and of a query: (upper, lower) columns; (third, none)
-  static constexpr int kSets = kF32 ? 2 : 1, kSetsQ = 2;
+  // products for the bytes of a weight: (upper, lower) columns; (third, none).  For those of the queries: NT of
+  // (upper, lower) columns, then the third bytes of two fragments as one
+  static constexpr int kSets = kF32 ? 2 : 1, kFragQ = NT + (NT + 1) / 2;
   // a query's largest number (signed bytes: 127 in each) and a weight's (unsigned)
   static constexpr int kTop = 127 * 65536 + 127 * 256 + 127;
   static constexpr int kTopW = kF32 ? 0x7fffff : 0xffff;
@@ -228,7 +229,7 @@ struct AttendCfg {
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
   static constexpr int kMerge = kAttWarps * kStreams * D * 4;
   static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kOffQs = kOffQ + kSetsQ * NT * kTp * (D / 32) * 32 * 8;
+  static constexpr int kOffQs = kOffQ + kFragQ * kTp * (D / 32) * 32 * 8;
   static constexpr int kOffMl = kOffQs + (kQ * (F::kGroups + 1) * 4 + 15) / 16 * 16;
   static constexpr int kOffEnt = kOffMl + kAttWarps * kStreams * 8;
   static_assert(kOffEnt % 16 == 0, "16-byte entries");
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kAttThreads, AttendCfg<TQ, D, GROUP, CW, NT>::
 cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   using F = Fmt<D, GROUP>;
-  constexpr int NG = F::kGroups, MT = C::kMt, SETS = C::kSets, SQ = C::kSetsQ, TP = C::kTp, ST = C::kSt, SF = C::kSf;
+  constexpr int NG = F::kGroups, MT = C::kMt, SETS = C::kSets, FQ = C::kFragQ, TP = C::kTp, ST = C::kSt, SF = C::kSf;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int abort_flag;
@@ -433,9 +434,9 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   }
   __syncthreads();
   start();
-  // B operands of K's products: columns 2 k, 2 k + 1 of a fragment are the upper and lower byte (the third
-  // byte and nothing, in the second set) of slot k = i CW + c, that is of query column c for tile i, and
-  // zero for the other tiles; word w covers dims 32 w .. 32 w + 31.  Bytes are signed, so a lower
+  // B operands of K's products: columns 2 k, 2 k + 1 of a fragment are the upper and lower byte (behind
+  // those, of fragments nt and nt + 1 the third byte) of slot k = i CW + c, that is of query column c for tile i,
+  // and zero for the other tiles; word w covers dims 32 w .. 32 w + 31.  Bytes are signed, so a lower
   // byte is -128..127 and the rest is rounded to it.
   for (int i = tid; i < NT * (D / 32) * 32; i += kAttThreads) {
     const int l = i & 31, w = (i >> 5) % (D / 32), nt = (i >> 5) / (D / 32);
@@ -443,9 +444,8 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     const bool lower = (l >> 2) & 1;
     const float step = qstep[cc];
     const float inv = step > 0.f ? 1.f / step : 0.f;
-    uint32_t v[SQ][2];
-#pragma unroll
-    for (int p = 0; p < SQ; ++p) v[p][0] = v[p][1] = 0u;
+    const bool third = lower == (nt & 1);  // this lane's column of the third bytes
+    uint32_t v[2][2] = {{0u, 0u}, {0u, 0u}};
     if (col < a.cols) {
       const TQ* q = q_row(col) + 32 * w + 2 * (l & 3);
 #pragma unroll
@@ -457,18 +457,20 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           const float y = inv < INFINITY ? x * inv : x / step;
           int f = max(-C::kTop, min(C::kTop, __float2int_rn(y)));
           const int b0 = (int8_t)f;  // the third byte
-          if (!lower) v[1][e] |= (uint32_t)(b0 & 255) << (8 * j);
+          if (third) v[1][e] |= (uint32_t)(b0 & 255) << (8 * j);
           f = (f - b0) >> 8;
           const int b1 = (int8_t)f, b2 = (f - b1) >> 8;
           v[0][e] |= (uint32_t)((lower ? b1 : b2) & 255) << (8 * j);
         }
     }
-#pragma unroll
-    for (int p = 0; p < SQ; ++p)
+    auto put = [&](int frag, const uint32_t (&u)[2]) {
 #pragma unroll
       for (int t = 0; t < TP; ++t)
-        reinterpret_cast<uint2*>(qf + (((p * NT + nt) * TP + t) * (D / 64) + (w >> 1)) * 32 + l)[w & 1] =
-            k / CW == t ? make_uint2(v[p][0], v[p][1]) : make_uint2(0u, 0u);
+        reinterpret_cast<uint2*>(qf + ((frag * TP + t) * (D / 64) + (w >> 1)) * 32 + l)[w & 1] =
+            k / CW == t ? make_uint2(u[0], u[1]) : make_uint2(0u, 0u);
+    };
+    put(nt, v[0]);
+    if (third || (nt % 2 == 0 && nt + 1 == NT)) put(NT + nt / 2, v[1]);  // (an unpaired column: zero)
   }
   __syncthreads();
 
@@ -530,7 +532,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     float s[SF][NT][2];
 #pragma unroll
     for (int f = 0; f < SF; ++f) {
-      int part[SQ][NT][NG][4];
+      int part[FQ][NG][4];
 #pragma unroll
       for (int i = 0; i < TP; ++i) {
         const uint8_t* tb = buf + (f * TP + i) * F::kTile;  // (a missing tile's sums are replaced below)
@@ -548,18 +550,15 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
             y[e][3] = (wb[w + e] >> 4) & 0x0f0f0f0fu;
           }
 #pragma unroll
-          for (int p = 0; p < SQ; ++p)
+          for (int p = 0; p < FQ; ++p) {
+            const uint4 q = qf[((p * TP + i) * (D / 64) + w / 2) * 32 + lane];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint4 q = qf[(((p * NT + nt) * TP + i) * (D / 64) + w / 2) * 32 + lane];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int n = (w + e) * 32 / GROUP;
-                const bool fresh = i == 0 && (w + e) * 32 % GROUP == 0;
-                imma16832<true>(part[p][nt][n], fresh, 0, y[e][0], y[e][1], y[e][2], y[e][3],
-                                e ? q.z : q.x, e ? q.w : q.y);
-              }
+            for (int e = 0; e < 2; ++e) {
+              const int n = (w + e) * 32 / GROUP;
+              const bool fresh = i == 0 && (w + e) * 32 % GROUP == 0;
+              imma16832<true>(part[p][n], fresh, 0, y[e][0], y[e][1], y[e][2], y[e][3], e ? q.z : q.x, e ? q.w : q.y);
             }
+          }
         }
       }
       const int mine = f * TP + my_tile;
@@ -578,8 +577,8 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             // at most 64 * 15 * 2^15; the third byte joins in float
-            float v = (float)(part[0][nt][n][2 * r] * 256 + part[0][nt][n][2 * r + 1]);
-            v = fmaf(v, 256.f, (float)part[1][nt][n][2 * r]);
+            float v = (float)(part[nt][n][2 * r] * 256 + part[nt][n][2 * r + 1]);
+            v = fmaf(v, 256.f, (float)part[NT + nt / 2][n][2 * r + nt % 2]);
             acc[nt][r] = fmaf(sc, v, acc[nt][r]);
             zero[nt][r] = fmaf(ze, qsum[nt][n], zero[nt][r]);
           }
