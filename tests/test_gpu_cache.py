@@ -394,12 +394,15 @@ def test_attend_many_splits(shape):
     assert torch.equal(out, again)  # no atomics: the same sums in the same order
 
 
-def test_attend_wide_table_short_sequence():
-    """A table with room for far more than the sequence holds (entries behind it are garbage)."""
-    c = Cache(30, B=2, H=2, ctx=(77, 130))
+@pytest.mark.parametrize("G", [1, 9, 16, 17, 40])
+@pytest.mark.parametrize("D,group", [(128, 64), (64, 32)])
+def test_attend_wide_table_short_sequence(G, D, group):
+    """A table with room for far more than the sequence holds (entries behind it are garbage); that also takes
+    the kernel for much work, with up to 16 columns at a time."""
+    c = Cache(30, B=2, H=2, D=D, group=group, ctx=(77, 130))
     wide = torch.full((2, 4096), 1 << 30, dtype=torch.int32, device=DEV)
     wide[:, :c.max_pages] = c.table
-    q = c.rand(2, 2, 1, 128).to(DEV)
+    q = c.rand(2, 2 * G, 1, D).to(DEV)
     out, lse = lsh.lsh_cache_attend(q, c.cache, wide, c.ctx_len, **c.form)
     assert _status() == 0
     _check_attend(c, q, out, lse, [1, 1])
