@@ -758,3 +758,32 @@ def test_binding_checks_on_the_device():
         lsh.lsh_cache_attend(q, c.cache, table, c.ctx_len, workspace=torch.empty(16, dtype=torch.uint8, device=DEV),
                              **c.form)
     assert _status() == 0
+
+
+@pytest.mark.parametrize("page,n_rounds,G,T", [(64, 4, 1, 1), (64, 8, 1, 2), (128, 8, 1, 1), (32, 8, 1, 1), (64, 16, 1, 3),
+                                              (64, 8, 2, 1), (64, 6, 1, 1)])
+def test_select_with_its_own_scoring_kernel(page, n_rounds, G, T):
+    """More tags a head than the choice scores itself: whole batches of pages, a cut one, a missing one."""
+    n = 701 * page - 5 if page < 128 else 333 * page + 1
+    n_pages = -(-n // page)
+    g = torch.Generator().manual_seed(page + n_rounds)
+    tags = torch.randint(0, 40, (n_pages + 1, 2, n_rounds, page), generator=g, dtype=torch.int16)
+    table = torch.randperm(n_pages, generator=g).to(torch.int32)[None]
+    qb = torch.randint(0, 40, (1, 2 * G, n_rounds, T), generator=g, dtype=torch.int32)
+    ctx = torch.tensor([n], dtype=torch.int32, device=DEV)
+    logical = tags[table[0].long()].permute(1, 2, 0, 3).reshape(2, n_rounds, -1)[:, :, :n].numpy().copy()
+    for bad_page, bad_bucket in ((False, False), (True, False), (False, True)):
+        tb, q, lg = table.clone(), qb.clone(), logical.copy()
+        if bad_page:
+            tb[0, 17] = n_pages + 9
+            lg[:, :, 17 * page:18 * page] = -1
+        if bad_bucket:
+            q[0, 0, 0, 0] = 70000
+        sel, scores = lsh.lsh_cache_select(tags.to(DEV), q.to(DEV), tb.to(DEV), ctx, 40, n_local=2)
+        for h in range(2):
+            for t in range(T):
+                want, ws = co.oracle_cache_select(lg[h], q[0, h * G:(h + 1) * G, :, t].numpy(), n - T + t, n, page,
+                                                  n_pages, 40, 2, True)
+                assert scores[0, h, t].tolist() == ws
+                assert sel[0, h, t].tolist() == want
+        assert _status() == (INVALID if bad_page else 0)
