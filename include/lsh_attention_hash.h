@@ -406,8 +406,8 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *              (other streams, graphs replayed at the same time) need one each
  *
  * The products with the codes are exact integer sums of fixed-point numbers: a query in steps of
- * its largest entry / 8355711, a weight in steps of the largest of its 64 keys' weights / 65535
- * (fp32 queries: / 8388607).  A query row with an infinity or a NaN answers NaN; stored values may
+ * its largest entry / 8355711, a weight (softmax numerator times the value's scale) in steps of 2^-22 of
+ * the power of two at or below the largest of its 64 keys' weights.  A query row with an infinity or a NaN answers NaN; stored values may
  * reach 1e36 (beyond that a weight times a scale can overflow).  Everything else is fp32; keys in any order give the same
  * result only up to rounding, the same call the same bits.
  * lse makes the result joinable with other key sets by lsh_combine_rounds, where one of

@@ -66,33 +66,24 @@ struct AttendPlan {
 
 constexpr int kMaxCtasPerSm = 6;
 
-inline AttendPlan attend_plan(int dtype, int B, int H, int G, int T, int D, int max_pages, int page, int n_select) {
+inline AttendPlan attend_plan(int B, int H, int G, int T, int D, int max_pages, int page, int n_select) {
   AttendPlan p;
   const bool sel = n_select > 0;
   p.units = (long long)B * H * (sel ? T : 1);
   p.cols = sel ? G : G * T;
-  // one or two columns: four or two tiles share a fragment; beyond four, fragments side by side, so
-  // that a cached token is unpacked once for up to 16 columns (8 heads of 64K, D 128: 16 queries take
-  // 264 us that way and four times 110 us by fours).  fp32 and D 256 have registers for two
-  // fragments, fp32 at D 256 for one (the second would spill 1.9 KB a thread).
-  const int most = D == 256 ? (dtype == LSH_F32 ? 1 : 2) : (dtype == LSH_F32 ? 2 : 4);
+  // one or two columns: four or two tiles share a fragment; beyond four, two fragments side by side, so that a
+  // cached token is unpacked once for up to 8 columns.  16 queries of 64 heads of 64K, D 128: 305 us so, 309 us with
+  // four fragments, whose sums do not fit the registers.  At D 256 two do not either (8 queries of 32 heads
+  // of 64K: 297 us, with one 285 us).
+  const int most = D == 256 ? 1 : 2;
   p.cw = p.cols >= 3 ? 4 : p.cols == 2 ? 2 : 1;
-  p.nt = p.cols <= 4 ? 1 : p.cols <= 8 ? std::min(2, most) : most;
+  p.nt = p.cols <= 4 ? 1 : most;
   const long long keys = (long long)(sel ? n_select : max_pages) * page;
   p.direct = keys <= 1024;
   const int block = lsh::cache::kBlockTiles * lsh::cache::kTileTokens;
   const int sms = dev_info().sms > 0 ? dev_info().sms : 148;
-  const auto tiles = [&]() {
-    p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
-    p.blocks = p.units * p.n_ct * ((keys + block - 1) / block);
-  };
-  tiles();
-  // four fragments are 7 % quicker than twice two where a CTA has many blocks (64 heads of 64K), and slower
-  // where it has few, as set-up and the last stage weigh more (32 heads of 8K: 54 us and 40 us)
-  if (p.nt == 4 && p.blocks < 16ll * 2 * sms) {
-    p.nt = 2;
-    tiles();
-  }
+  p.n_ct = (p.cols + p.cw * p.nt - 1) / (p.cw * p.nt);
+  p.blocks = p.units * p.n_ct * ((keys + block - 1) / block);
   p.max_ctas = (int)std::max<long long>(1, std::min<long long>(p.blocks, (long long)sms * kMaxCtasPerSm));
   return p;
 }
@@ -299,7 +290,7 @@ size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, 
                                         int n_select) {
   if (!valid_dtype(dtype) || check_cache_form(H, D, page, 32, 1, B, max_pages) != LSH_OK) return 0;
   if (H <= 0 || Hq <= 0 || Hq % H != 0 || T <= 0 || B <= 0 || n_select < 0) return 0;
-  return attend_plan_bytes(attend_plan(dtype, B, H, Hq / H, T, D, max_pages, page, n_select), D);
+  return attend_plan_bytes(attend_plan(B, H, Hq / H, T, D, max_pages, page, n_select), D);
 }
 
 lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int T, int D, const void* cache,
@@ -322,7 +313,7 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
       !aligned16(lse) || (new_len && !aligned16(new_len)) || (selected && !aligned16(selected)))
     return LSH_ERR_ALIGN;
   if ((long long)B * Hq * T == 0) return LSH_OK;
-  const AttendPlan p = attend_plan(dtype, B, H, Hq / H, T, D, max_pages, page, n_select);
+  const AttendPlan p = attend_plan(B, H, Hq / H, T, D, max_pages, page, n_select);
   if (p.units * p.cols >= (1ll << 31) || p.units * p.n_ct >= (1ll << 31)) return LSH_ERR_SHAPE;
   const size_t need = attend_plan_bytes(p, D);
   if (need > 0 && (!workspace || workspace_bytes < need)) return LSH_ERR_WORKSPACE;
@@ -357,15 +348,12 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
     if (p.cw == 1) return launch_cache_attend<TQ, DD, GG, 1, 1>(a, p, s);       \
     if (p.cw == 2) return launch_cache_attend<TQ, DD, GG, 2, 1>(a, p, s);       \
     if (p.nt == 1) return launch_cache_attend<TQ, DD, GG, 4, 1>(a, p, s);       \
+    if constexpr (DD <= 128) return launch_cache_attend<TQ, DD, GG, 4, 2>(a, p, s); \
   } while (0)
-    if (dtype == LSH_F32) {
+    if (dtype == LSH_F32)
       LSH_CA(float);
-      if constexpr (DD <= 128) return launch_cache_attend<float, DD, GG, 4, 2>(a, p, s);
-    } else {
+    else
       LSH_CA(bf);
-      if (p.nt == 2) return launch_cache_attend<bf, DD, GG, 4, 2>(a, p, s);
-      if constexpr (DD <= 128) return launch_cache_attend<bf, DD, GG, 4, 4>(a, p, s);
-    }
 #undef LSH_CA
     return LSH_ERR_UNSUPPORTED;
   });

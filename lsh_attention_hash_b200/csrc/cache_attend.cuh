@@ -16,15 +16,18 @@
 //   K: the query is a fixed-point number of 24 bits of the column's largest |q|.  The sums are
 //      exact; the rounding of q is 2^-24 of its largest entry.  (16 bits would save a product in
 //      three, but their rounding, the same for every key, moves the log-sum-exp by 1e-4.)
-//   V: the weights p_j s_j of a stage's 64 keys are fixed-point numbers of the largest of them,
-//      16 bits for bf16 queries and 23 for fp32 ones; the sums go into float accumulators
-//      after every stage.  A scale for each stage and not for the whole sequence: however many
+//   V: the weights p_j s_j of a stage's 64 keys are fixed-point numbers in steps of 2^(e - 22), 2^e the
+//      power of two at or below the largest of them: 22 to 23 bits, as much as float products keep, and a weight
+//      with a short mantissa (a lone key's is its scale) is exact.  (16 bits save a product in three; the
+//      outputs were then off by 3e-4 of their size, so that one bf16 result in fifty was rounded to its
+//      neighbour.)  The sums go into float accumulators after every stage.  A step for each
+//      stage and not for the whole sequence: however many
 //      small weights there are, what rounding takes from a stage is at most 64 half steps of its
 //      own largest weight.  The upper nibbles stay where they are (16 c); their scale takes
 //      the 16 out.  An accumulator that starts at 0x4B400000 is, read as a float, 1.5 * 2^23
 //      plus the sum, so the integers become floats by one subtraction.
 //
-// A number's two upper bytes are two columns of the product (a third byte is a second product), so a
+// A number's two upper bytes are two columns of the product (the third bytes of two fragments are a product more), so a
 // fragment's 8 columns are 4 numbers: CW queries of each of TP = 4 / CW tiles, tile i's
 // products using a B operand that is zero outside its own columns.  A single query thus
 // fills all lanes: lane 4 g + t4 has keys g and g + 8 of tile t4, and scales, exponentials and
@@ -212,12 +215,11 @@ struct AttendCfg {
   using F = Fmt<D, GROUP>;
   static_assert(CW == 4 || NT == 1, "more than 4 queries go in whole fragments");
   static constexpr bool kF32 = sizeof(TQ) == 4;
-  // products for the bytes of a weight: (upper, lower) columns; (third, none).  For those of the queries: NT of
-  // (upper, lower) columns, then the third bytes of two fragments as one
-  static constexpr int kSets = kF32 ? 2 : 1, kFragQ = NT + (NT + 1) / 2;
-  // a query's largest number (signed bytes: 127 in each) and a weight's (unsigned)
+  // products for the bytes of queries or weights: NT of (upper, lower) columns, then the third bytes of two
+  // fragments as one
+  static constexpr int kFrag = NT + (NT + 1) / 2;
+  // a query's largest number: signed bytes, 127 in each
   static constexpr int kTop = 127 * 65536 + 127 * 256 + 127;
-  static constexpr int kTopW = kF32 ? 0x7fffff : 0xffff;
   static constexpr int kMt = D / 16;       // m tiles of V^T P^T
   static constexpr int kTp = 4 / CW;       // tiles of a fragment
   static constexpr int kSt = 4;            // tiles of a stage
@@ -229,7 +231,7 @@ struct AttendCfg {
   static constexpr int kRing = kAttWarps * kStages * kStageBytes;
   static constexpr int kMerge = kAttWarps * kStreams * D * 4;
   static constexpr int kOffQ = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kOffQs = kOffQ + kFragQ * kTp * (D / 32) * 32 * 8;
+  static constexpr int kOffQs = kOffQ + kFrag * kTp * (D / 32) * 32 * 8;
   static constexpr int kOffMl = kOffQs + (kQ * (F::kGroups + 1) * 4 + 15) / 16 * 16;
   static constexpr int kOffEnt = kOffMl + kAttWarps * kStreams * 8;
   static_assert(kOffEnt % 16 == 0, "16-byte entries");
@@ -238,7 +240,7 @@ struct AttendCfg {
   static constexpr int kSmem = kOffBar + kAttWarps * kStages * 8;
   static_assert(kBlockTiles % kSt == 0, "blocks are whole stages");
   // CTAs of an SM: what registers allow (128 threads each) and what shared memory does
-  static constexpr int kByRegs = NT == 4 || D == 256 ? 2 : D == 64 ? 4 : 3;
+  static constexpr int kByRegs = D == 256 ? 2 : D == 64 ? 4 : 3;
   static constexpr int kBySmem = 227 * 1024 / (kSmem + 1024);
   static constexpr int kCtas = kByRegs < kBySmem ? kByRegs : kBySmem;
 };
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kAttThreads, AttendCfg<TQ, D, GROUP, CW, NT>::
 cache_attend_kernel(const __grid_constant__ AttendArgs a) {
   using C = AttendCfg<TQ, D, GROUP, CW, NT>;
   using F = Fmt<D, GROUP>;
-  constexpr int NG = F::kGroups, MT = C::kMt, SETS = C::kSets, FQ = C::kFragQ, TP = C::kTp, ST = C::kSt, SF = C::kSf;
+  constexpr int NG = F::kGroups, MT = C::kMt, FQ = C::kFrag, TP = C::kTp, ST = C::kSt, SF = C::kSf;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int abort_flag;
@@ -631,74 +633,82 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         for (int n = 0; n < NG; ++n) zs[nt][n] *= al;
       }
     }
-    // ---- weights p s: their largest of the stage, then fixed-point numbers of it
-    float wt[SF][NT][NG][2];
-    uint32_t top_w[NT][NG];  // bits of a float that is not negative order as integers do, NaN above all
+    // ---- weights p, and what they take from the zeros
+    float p[SF][NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int n = 0; n < NG; ++n) top_w[nt][n] = 0u;
-#pragma unroll
-    for (int f = 0; f < SF; ++f) {
-      float p[NT][2];
+    for (int f = 0; f < SF; ++f)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float y = s[f][nt][r] - base[nt];
-          p[nt][r] = C::kF32 ? exp2f(y) : tc::ex2_approx(y);
-          l[nt] += p[nt][r];
+          p[f][nt][r] = C::kF32 ? exp2f(y) : tc::ex2_approx(y);
+          l[nt] += p[f][nt][r];
         }
-      const uint32_t* vp = reinterpret_cast<const uint32_t*>(buf + (f * TP + my_tile) * F::kTile + F::kOffVp);
+    // ---- O += weights . codes, 64 dims at a time: p s of their groups, the largest of the stage, fixed-point
+    // numbers of it, then 16 dims of 64 keys in a product
+    constexpr int NQ = 64 / GROUP;  // groups of 64 dims
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+    for (int q = 0; q < D / 64; ++q) {
+      float unit[NT][NQ];              // what a step of the weights is worth
+      uint32_t pb[SF][NQ][FQ];         // their bytes in column g: keys 2 t4, +1, 2 t4 + 8, +9 of the column's tile
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const uint32_t pw = vp[n * 16 + g + 8 * r];
-          const float sc = bf16_bits(pw), ze = __uint_as_float(pw & 0xffff0000u);
+      for (int u = 0; u < NQ; ++u) {
+        const int n = q * NQ + u;
+        float wt[SF][NT][2];
+        uint32_t top_w[NT];  // bits of a float that is not negative order as integers do, NaN above all
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const bool out = MASKED && s[f][nt][r] == -INFINITY;  // whatever lies in a masked place
-            const float w = out ? 0.f : p[nt][r] * sc;
-            if (!out) zs[nt][n] = fmaf(p[nt][r], ze, zs[nt][n]);
-            wt[f][nt][n][r] = w;
-            top_w[nt][n] = max(top_w[nt][n], __float_as_uint(w));
-          }
-        }
-    }
-    float unit[NT][NG];                // what a step of the weights is worth
-    uint32_t pb[SF][NT][NG][SETS];     // their bytes in column g: keys 2 t4, +1, 2 t4 + 8, +9 of the column's tile
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        uint32_t t = top_w[nt][n];
-        t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
-        t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
-        t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
-        const float wm = __uint_as_float(t);
-        unit[nt][n] = wm * (1.f / C::kTopW);
-        // weights below 2^-110 are nothing (a value's scale is 2^-100 at least); NaN and infinity stay
-        // in the unit; both sides 2^-16 smaller, as the quick division's divisor ends at 2^126
-        constexpr float k16 = 1.f / 65536.f;
-        const float inv = wm > 7.7037197775489434e-34f ? __fdividef((float)C::kTopW * k16, wm * k16) : 0.f;
+        for (int nt = 0; nt < NT; ++nt) top_w[nt] = 0u;
 #pragma unroll
         for (int f = 0; f < SF; ++f) {
-          uint32_t x[2];  // the number in the low bits of a float's mantissa
+          const uint32_t* vp = reinterpret_cast<const uint32_t*>(buf + (f * TP + my_tile) * F::kTile + F::kOffVp);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) x[r] = __float_as_uint(fmaf(wt[f][nt][n][r], inv, 8388608.f));
-          // a number's bytes as the two columns of its slot
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t pw = vp[n * 16 + g + 8 * r];
+            const float sc = bf16_bits(pw), ze = __uint_as_float(pw & 0xffff0000u);
 #pragma unroll
-          for (int e = 0; e < SETS; ++e) {
-            const uint32_t pick = SETS == 1 ? 0x4041 : e == 0 ? 0x4142 : 0x4440;
-            const uint32_t lo = movmatrix(__byte_perm(x[0], 0u, pick)), hi = movmatrix(__byte_perm(x[1], 0u, pick));
-            pb[f][nt][n][e] = __byte_perm(lo, hi, 0x6420);
+            for (int nt = 0; nt < NT; ++nt) {
+              const bool out = MASKED && s[f][nt][r] == -INFINITY;  // whatever lies in a masked place
+              const float w = out ? 0.f : p[f][nt][r] * sc;
+              if (!out) zs[nt][n] = fmaf(p[f][nt][r], ze, zs[nt][n]);
+              wt[f][nt][r] = w;
+              top_w[nt] = max(top_w[nt], __float_as_uint(w));
+            }
+          }
+        }
+        float inv[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t t = top_w[nt];
+          t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
+          t = max(t, __shfl_xor_sync(0xffffffffu, t, 8));
+          t = max(t, __shfl_xor_sync(0xffffffffu, t, 16));
+          // with 2^e the power of two at or below the largest, 2^-105 at least: a step is 2^(e - 22), so numbers end at
+          // 2^23; unit is the step times 2^16, and NaN where the largest is NaN or infinite
+          const uint32_t e = max(t & 0x7f800000u, 22u << 23);
+          inv[nt] = __uint_as_float((276u << 23) - e);
+          unit[nt][u] = __uint_as_float(e == 0x7f800000u ? 0x7fffffffu : e - (6u << 23));
+        }
+#pragma unroll
+        for (int f = 0; f < SF; ++f) {
+          uint32_t x[NT][2];  // the number in the low bits of a float's mantissa (2^23 itself: as 0x4B800000, the same bytes)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) x[nt][r] = __float_as_uint(fmaf(wt[f][nt][r], inv[nt], 8388608.f));
+          // its bytes as columns: the upper two as those of its slot, the lowest beside another fragment's.  (What
+          // stands in the odd bytes goes no further.)
+          auto column = [&](uint32_t lo, uint32_t hi) { return __byte_perm(movmatrix(lo), movmatrix(hi), 0x6420); };
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            pb[f][u][nt] = column(__byte_perm(x[nt][0], 0u, 0x4142), __byte_perm(x[nt][1], 0u, 0x4142));
+#pragma unroll
+          for (int nt = 0; nt < NT; nt += 2) {
+            const uint32_t y0 = nt + 1 < NT ? x[nt + (nt + 1 < NT)][0] : 0u, y1 = nt + 1 < NT ? x[nt + (nt + 1 < NT)][1] : 0u;
+            pb[f][u][NT + nt / 2] = column(__byte_perm(x[nt][0], y0, 0x4400), __byte_perm(x[nt][1], y1, 0x4400));
           }
         }
       }
-    // ---- O += weights . codes, 16 dims of 64 keys at a time
-#pragma unroll
-    for (int q = 0; q < D / 64; ++q) {
       uint32_t by[ST][4];  // byte j of the four keys of a lane: dims 16 j + g (low nibble), 16 j + 8 + g
 #pragma unroll
       for (int k = 0; k < ST; ++k) {
@@ -713,30 +723,28 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int mt = 4 * q + j, n = mt * 16 / GROUP;
-        int sum[SETS][NT][4];
+        const int mt = 4 * q + j, u = j * 16 / GROUP;
+        int sum[FQ][4];
 #pragma unroll
         for (int k = 0; k < ST; k += 2) {  // two tiles: the depth of a product
           const uint32_t a0 = by[k][j] & 0x0f0f0f0fu, a1 = by[k][j] & 0xf0f0f0f0u;
           const uint32_t a2 = by[k + 1][j] & 0x0f0f0f0fu, a3 = by[k + 1][j] & 0xf0f0f0f0u;
 #pragma unroll
-          for (int e = 0; e < SETS; ++e)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              // a tile's own columns only
-              const uint32_t b0 = TP == 1 || (g >> 1) / CW == k % TP ? pb[k / TP][nt][n][e] : 0u;
-              const uint32_t b1 = TP == 1 || (g >> 1) / CW == (k + 1) % TP ? pb[(k + 1) / TP][nt][n][e] : 0u;
-              imma16832<false>(sum[e][nt], k == 0, 0x4B400000, a0, a1, a2, a3, b0, b1);
-            }
+          for (int e = 0; e < FQ; ++e) {
+            // a tile's own columns only
+            const uint32_t b0 = TP == 1 || (g >> 1) / CW == k % TP ? pb[k / TP][u][e] : 0u;
+            const uint32_t b1 = TP == 1 || (g >> 1) / CW == (k + 1) % TP ? pb[(k + 1) / TP][u][e] : 0u;
+            imma16832<false>(sum[e], k == 0, 0x4B400000, a0, a1, a2, a3, b0, b1);
+          }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float v = fmaf(__int_as_float(sum[0][nt][2 * r]) - 12582912.f, 256.f,
-                           __int_as_float(sum[0][nt][2 * r + 1]) - 12582912.f);
-            if (SETS == 2) v = fmaf(v, 256.f, __int_as_float(sum[SETS - 1][nt][2 * r]) - 12582912.f);
-            o[nt][mt][r] = fmaf(v, unit[nt][n] * (r ? 0.0625f : 1.f), o[nt][mt][r]);  // upper nibbles: 16 c
+            float v = fmaf(__int_as_float(sum[NT + nt / 2][2 * r + nt % 2]) - 12582912.f, 1.f / 256.f,
+                           __int_as_float(sum[nt][2 * r + 1]) - 12582912.f);
+            v = fmaf(v, 1.f / 256.f, __int_as_float(sum[nt][2 * r]) - 12582912.f);
+            o[nt][mt][r] = fmaf(v, unit[nt][u] * (r ? 0.0625f : 1.f), o[nt][mt][r]);  // upper nibbles: 16 c
           }
       }
     }

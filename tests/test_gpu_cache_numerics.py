@@ -1,0 +1,101 @@
+"""How exactly attention over the cache and its storage answer: bounds tighter than the output's rounding, and
+sizes of keys, values and lengths at the ends of what the entry points promise."""
+
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+import lsh_attention_hash_b200 as lsh
+from oracle import cache_oracle as co
+from tests.test_gpu_cache import DEV, Cache, _status, np64
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [(64, 32, 16), (64, 64, 128), (128, 32, 32), (128, 64, 64), (256, 64, 64), (256, 32, 256)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,group,page", FORMS)
+@pytest.mark.parametrize("G,wide", [(1, False), (1, True), (2, False), (8, True), (17, True)])
+def test_a_lone_key_gives_its_stored_value(dtype, D, group, page, G, wide):
+    """Softmax over one key is 1: the output is the stored value, rounded once.
+
+    The weight 1 * s and its products with codes are exact (8 + 4 bits), the zero joins in float: z + s c has one
+    rounding to 24 bits, as the oracle's value has on its way to float32; bf16 rounds that once more.
+    """
+    c = Cache(80, dtype=dtype, B=2, H=2, D=D, group=group, page=page, ctx=(1, 1))
+    table = torch.full((2, 2048 // page + 1), 1 << 30, dtype=torch.int32, device=DEV) if wide else c.table.clone()
+    table[:, :1] = c.table
+    q = c.rand(2, 2 * G, 1, D, dtype=dtype).to(DEV)
+    for out_dtype in (torch.float32, torch.bfloat16):
+        out, _ = lsh.lsh_cache_attend(q, c.cache, table, c.ctx_len, unit_keys=False, out_dtype=out_dtype, **c.form)
+        for b in range(2):
+            for h in range(2):
+                want = torch.from_numpy(c.stored(b, h)[1][0].astype(np.float32)).to(out_dtype)
+                assert torch.equal(out[b, h * G:(h + 1) * G, 0].cpu(), want.expand(G, D))
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,group,page", FORMS)
+@pytest.mark.parametrize("G,wide", [(1, False), (2, True), (4, False), (16, True)])
+def test_weights_keep_the_precision_of_floats(dtype, D, group, page, G, wide):
+    """A few keys of very different weights, plain keys, float32 answers to either type of query.
+
+    A weight p s is a whole number of steps of at most 2^-22 of the largest one, so n keys' roundings take n half
+    steps times a code of 15 at most: n * 15 * 2^-23 of the largest p s.  Of the logits: half a step of the
+    query (its largest entry / 8355711) per dim, and what float does to parts of their sizes, 2^-20; the
+    exponential's argument is rounded to 2^-24 of its size and the result to 2^-22.  Sums of n floats: n 2^-24.
+    """
+    n = 20
+    c = Cache(81, dtype=dtype, B=1, H=2, D=D, group=group, page=page, ctx=(n,))
+    table = torch.full((1, 2048 // page + 1), 1 << 30, dtype=torch.int32, device=DEV) if wide else c.table.clone()
+    table[:, :c.max_pages] = c.table
+    q = (c.rand(1, 2 * G, 1, D) * 2).to(dtype).to(DEV)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, table, c.ctx_len, unit_keys=False, self_mask=False,
+                                    out_dtype=torch.float32, **c.form)
+    for hq in range(2 * G):
+        h = hq // G
+        K, V, inv = c.stored(0, h)
+        _, _, zk = co.oracle_quantise(np64(c.k[0, h, :n]), group)
+        _, sv, zv = co.oracle_quantise(np64(c.v[0, h, :n]), group)
+        zK, zV, sV = (np.repeat(x, group, axis=1) for x in (zk, zv, sv))
+        x = np64(q[0, hq, 0])
+        want, wl, w, _ = co.oracle_cache_attend_row(x, K, V, inv, n - 1, n, None, page, False, True, False, None)
+        code = np.abs(K - zK)
+        dz = (0.5 * np.abs(x).max() / 8355711 * code.sum(1) + 2.0 ** -20 * ((code + np.abs(zK)) @ np.abs(x))) / np.sqrt(D)
+        z = K @ x / np.sqrt(D)
+        rel = 2 * dz.max() + np.abs(z - z.max()).max() * 2.0 ** -23 + 2.0 ** -21 + n * 2.0 ** -23
+        bound = n * 15 * 2.0 ** -23 * (w[:, None] * sV).max(0) + rel * (w @ (np.abs(V - zV) + np.abs(zV)))
+        err = np.abs(np64(out[0, hq, 0]) - want)
+        assert (err <= bound).all(), (hq, (err / bound).max())
+        assert abs(float(lse[0, hq, 0]) - wl) <= rel + 2.0 ** -22 * abs(wl)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,group,page", FORMS)
+@pytest.mark.parametrize("G", [1, 2, 4, 16])
+def test_small_weights_beside_a_large_one(dtype, D, group, page, G):
+    """Equal probabilities, one key with a scale 2^10 times the others' but codes of 0 in all but a dim.
+
+    Logits are 0 and probabilities 1 exactly, so the weights are the scales.  n keys are off by n half steps of 2^-22
+    of the largest scale, 1, times a code of 15; the rest is sums of n floats, n 2^-23 of their sizes.
+    """
+    n = 20
+    g = torch.Generator().manual_seed(82)
+    v = torch.rand(1, 2, n, D, generator=g) * 15 * 2.0 ** -10
+    v[:, :, 7] = 0.0
+    v[:, :, 7, ::group] = 15.0
+    k = torch.randn(1, 2, n, D, generator=g)
+    c = Cache(82, B=1, H=2, D=D, group=group, page=page, ctx=(n,), rows=(k.to(dtype), v.to(dtype)))
+    q = torch.zeros(1, 2 * G, 1, D, dtype=dtype, device=DEV)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, self_mask=False, out_dtype=torch.float32, **c.form)
+    for h in range(2):
+        V = c.stored(0, h)[1]
+        bound = 15 * 2.0 ** -23 + n * 2.0 ** -23 * np.abs(V).mean(0)
+        err = np.abs(np64(out[0, h * G:(h + 1) * G, 0]) - V.mean(0))
+        assert (err <= bound).all(), (err / bound).max()
+    assert (lse.double() - np.log(n)).abs().max() <= 2.0 ** -22 * np.log(n)
