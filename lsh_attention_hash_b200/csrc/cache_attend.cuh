@@ -57,7 +57,9 @@
 
 #include <type_traits>
 
+#include "attend_tc.cuh"
 #include "cache_common.cuh"
+#include "cache_ring.cuh"
 #include "tc_common.cuh"
 
 namespace lsh {
@@ -169,6 +171,27 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                : "memory");
+}
+
+// Bounded wait for a stage's copies: true for the whole warp or for none of it, as its lanes go on to shuffles and
+// matrix products together.  (att_tc::warp_wait sleeps with a long hint: 2 % slower here, as copies are mostly there.)
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = tc::globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+    if ((i & 31u) == 0) {
+      int bail = 0;
+      if ((threadIdx.x & 31) == 0) {
+        bail = *abort_flag;
+        if (!bail && tc::globaltimer() - t0 > tc::kWaitNs) {
+          *abort_flag = bail = 1;
+          record_error(LSH_ERR_TIMEOUT);
+        }
+      }
+      if (__shfl_sync(0xffffffffu, bail, 0)) return false;
+    }
+  }
 }
 
 // d = (first ? start : d) + codes (unsigned bytes) times signed (BS) or unsigned bytes.
@@ -750,41 +773,31 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     }
   };
 
+  bool ok = true;  // whether every wait of this warp ended in time
   for (;;) {
-  const int n_stage = (tile1 - tile0 + ST - 1) / ST;
-  for (int st = warp; st < n_stage; st += kAttWarps) {
-    if (!tc::mbar_wait(bar + slot, phase, &abort_flag)) {
-      // give the copies in flight the same time each, then leave
-      for (int i = 0, s2 = slot; i < kStages; ++i) {
-        if (st + i * kAttWarps < n_stage) {
-          const unsigned long long t0 = tc::globaltimer();
-          while (!tc::mbar_try_wait(bar + s2, (s2 < slot) ? phase ^ 1 : phase) && tc::globaltimer() - t0 < tc::kWaitNs) {
-          }
-        }
-        s2 = s2 + 1 == kStages ? 0 : s2 + 1;
-      }
-      break;
-    }
-    const int4 at = desc[slot];
-    const int* first = reinterpret_cast<const int*>(desc + slot);
-    const int lo = min(min(at.x, at.y), min(at.z, at.w)), hi = max(max(at.x, at.y), max(at.z, at.w));
-    const uint8_t* buf = ring + slot * C::kStageBytes;
-    if (lo >= 0 && hi + kTileTokens <= fast)
-      consume(buf, first, std::false_type());
-    else if (hi >= 0)
-      consume(buf, first, std::true_type());
-    __syncwarp();
-    if (lane == 0 && st + kStages * kAttWarps < n_stage) issue(st + kStages * kAttWarps, slot);
-    if (++slot == kStages) {
-      slot = 0;
-      phase ^= 1;
-    }
-  }
-  if (tile1 >= tile_hi) break;
-  __syncthreads();
-  look_up();
-  __syncthreads();
-  start();
+    ok = run_stages<kStages, kAttWarps>(
+        warp, (tile1 - tile0 + ST - 1) / ST, slot, phase,
+        [&](int s, uint32_t parity) { return stage_wait(bar + s, parity, &abort_flag); },
+        [&](int s, uint32_t parity) { att_tc::drain_wait(bar + s, parity); },
+        [&](int, int s) {
+          const int4 at = desc[s];
+          const int* first = reinterpret_cast<const int*>(desc + s);
+          const int lo = min(min(at.x, at.y), min(at.z, at.w)), hi = max(max(at.x, at.y), max(at.z, at.w));
+          const uint8_t* buf = ring + s * C::kStageBytes;
+          if (lo >= 0 && hi + kTileTokens <= fast)
+            consume(buf, first, std::false_type());
+          else if (hi >= 0)
+            consume(buf, first, std::true_type());
+          __syncwarp();
+        },
+        [&](int st, int s) {
+          if (lane == 0) issue(st, s);
+        });
+    if (tile1 >= tile_hi) break;
+    if (__syncthreads_or(!ok)) return;  // a wait gave up (the status word says so): every warp leaves
+    look_up();
+    __syncthreads();
+    start();
   }
 
   // ---- join the warps -----------------------------------------------------------------------------
@@ -798,7 +811,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
     }
     if (g == 0) ml[warp * C::kStreams + nt * 4 + t4] = make_float2(m[nt], l[nt]);
   }
-  __syncthreads();  // the ring is free
+  if (__syncthreads_or(!ok)) return;  // (else the ring is free)
   float* om = reinterpret_cast<float*>(smem);  // [warp][stream][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
