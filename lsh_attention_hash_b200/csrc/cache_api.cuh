@@ -279,10 +279,13 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
   }
   const int smem = fused || max_pages > n_select ? std::max(16, (max_pages + 3) / 4 * 16) : 16;
   a.fused = fused;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(lsh::cache::cache_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-          cudaSuccess)
-    return LSH_ERR_CUDA;
+  if (smem > 32 * 1024) {
+    // 48 KB are free to use, the kernel's static shared memory among them; beyond, the largest choice's limit is set
+    // once: one for each call's size could be lowered by another thread's call before the launch
+    static std::atomic<uint64_t> done{0};
+    const lsh_status lim = allow_smem((const void*)lsh::cache::cache_pick_kernel, lsh::cache::kMaxPickPages * 4, done);
+    if (lim != LSH_OK) return lim;
+  }
   return launch_early(lsh::cache::cache_pick_kernel, (unsigned)rows, lsh::cache::kPickThreads, smem, s, a);
 }
 
