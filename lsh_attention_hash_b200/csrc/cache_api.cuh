@@ -101,7 +101,10 @@ inline lsh_status allow_smem(const void* fn, int bytes, std::atomic<uint64_t>& d
   if (cudaGetDevice(&dev) != cudaSuccess) return LSH_ERR_CUDA;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0;
   if (bit && (done.load(std::memory_order_relaxed) & bit)) return LSH_OK;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return LSH_ERR_CUDA;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();  // (reported here, not by whatever launches next)
+    return LSH_ERR_CUDA;
+  }
   done.fetch_or(bit, std::memory_order_relaxed);
   return LSH_OK;
 }
@@ -121,7 +124,9 @@ lsh_status launch_early(void (*fn)(Args), unsigned grid, int threads, int smem, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, fn, args) == cudaSuccess) return LSH_OK;
+  cudaGetLastError();  // (reported here, not by whatever launches next)
+  return LSH_ERR_CUDA;
 }
 
 template <typename TQ, int D, int GROUP, int CW, int NT>
@@ -276,6 +281,8 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
     else if (chunks == 2) lsh::cache::cache_score_kernel<2><<<grid, threads, 0, s>>>(a, groups);
     else if (chunks == 4) lsh::cache::cache_score_kernel<4><<<grid, threads, 0, s>>>(a, groups);
     else lsh::cache::cache_score_kernel<0><<<grid, threads, 0, s>>>(a, groups);
+    const lsh_status run = launch_status();
+    if (run != LSH_OK) return run;
   }
   const int smem = fused || max_pages > n_select ? std::max(16, (max_pages + 3) / 4 * 16) : 16;
   a.fused = fused;

@@ -69,3 +69,43 @@ def test_selects_of_several_threads():
     for t in threads:
         t.join()
     assert not wrong and _status() == 0
+
+
+@pytest.mark.parametrize("which", ["attend", "select", "select wide"])
+def test_a_refused_launch_is_reported_once(which):
+    """A launch that CUDA refuses (on the legacy stream while a blocking stream captures) is that call's error and
+    not also the next one's."""
+    import ctypes
+
+    rt = ctypes.CDLL("libcudart.so.12")
+    c = Cache(90, B=1, H=1, ctx=(40,), n_rounds=2)
+    q, k = c.rand(1, 1, 1, 128).to(DEV), c.k[:, :, -1:].contiguous().to(DEV)
+    out, lse = torch.empty_like(q), torch.empty(1, 1, 1, device=DEV)
+    pages = 1200 if which == "select wide" else c.max_pages  # (wide: its scoring kernel is refused, then its choice)
+    table = torch.zeros(1, pages, dtype=torch.int32, device=DEV)
+    qb = torch.zeros(1, 1, 2, 1, dtype=torch.int32, device=DEV)
+    sel, scores = (torch.empty(1, 1, 1, n, dtype=torch.int32, device=DEV) for n in (1, pages))
+
+    def call():
+        if which == "attend":
+            lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, out=out, lse=lse, **c.form)
+        else:
+            lsh.lsh_cache_select(c.tags, qb, table, c.ctx_len, 1, selected=sel, scores=scores)
+
+    call()
+    torch.cuda.synchronize()
+    s, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert torch.cuda.current_stream().cuda_stream == 0
+    assert rt.cudaStreamCreate(ctypes.byref(s)) == 0
+    assert rt.cudaStreamBeginCapture(s, 2) == 0  # relaxed
+    try:
+        with pytest.raises(lsh.LSHError, match="LSH_ERR_CUDA"):
+            call()
+    finally:
+        rt.cudaStreamEndCapture(s, ctypes.byref(graph))  # (the capture is void)
+        rt.cudaGetLastError()
+        rt.cudaStreamDestroy(s)
+    lsh.lsh_cache_write(k, k, c.cache, c.table, c.ctx_len, **c.form)
+    call()
+    torch.cuda.synchronize()
+    assert _status() == 0
