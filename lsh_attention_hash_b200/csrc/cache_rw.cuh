@@ -18,7 +18,7 @@
 //
 // Measured, 8 x 8 heads x 16384 rows: D 128 bf16 writing 196 us (3.5 TB/s: 610 instructions a warp for its
 // 1024 values bind it), reading 109 us (6.3 TB/s, 96 % of the measured copy rate); 8 heads x 262144 rows of 64 in
-// fp32: writing 219 us (5.6 TB/s), reading 191 us (6.5 TB/s).
+// fp32: writing 226 us (5.5 TB/s), reading 191 us (6.5 TB/s).
 #pragma once
 
 #include "cache_common.cuh"
@@ -301,6 +301,22 @@ struct WriteArgs {
   Pages pg;
 };
 
+// 1 / length of a row whose squares overflow a float (it is longer than 1.8e19), from the row scaled by 2^-96; 0 for a
+// row with an infinity, NaN for one with a NaN.  One lane reads the row again: the common case pays a comparison (bf16
+// nothing that shows, fp32 217 -> 226 us for 8 heads x 262144 rows of 64, as its registers are full; the whole warp by a vote 222,
+// but bf16 5 % more).
+template <typename T, int D>
+__device__ __noinline__ float long_row_inv(const T* row) {
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int d = 0; d < D; d += 8) {
+    float x[8];
+    load8(row + d, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = fmaf(x[i] * 0x1p-96f, x[i] * 0x1p-96f, s[i]);
+  }
+  return 1.f / sqrtf(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]))) * 0x1p-96f;
+}
+
 template <typename T, int D, int GROUP>
 __global__ void __launch_bounds__(kRwThreads, 4) cache_write_kernel(const WriteArgs a) {
   using F = Fmt<D, GROUP>;
@@ -335,7 +351,11 @@ __global__ void __launch_bounds__(kRwThreads, 4) cache_write_kernel(const WriteA
     reinterpret_cast<uint32_t*>(tile + F::kOffKp)[grp * 16 + t] = gk.word;
     reinterpret_cast<uint32_t*>(tile + F::kOffVp)[grp * 16 + t] = gv.word;
   }
-  if (j == 0) reinterpret_cast<float*>(tile + F::kOffInv)[t] = 1.f / fmaxf(sqrtf(sq), 1e-12f);
+  if (j == 0) {
+    float inv = 1.f / fmaxf(sqrtf(sq), 1e-12f);
+    if (!(sq < INFINITY)) inv = long_row_inv<T, D>(static_cast<const T*>(a.k) + (long long)row * D);
+    reinterpret_cast<float*>(tile + F::kOffInv)[t] = inv;
+  }
   if (a.tags) {
     const int page = 1 << a.pg.page_log2;
     for (int n = j; n < a.n_rounds; n += kLanes) {

@@ -99,3 +99,25 @@ def test_small_weights_beside_a_large_one(dtype, D, group, page, G):
         err = np.abs(np64(out[0, h * G:(h + 1) * G, 0]) - V.mean(0))
         assert (err <= bound).all(), (err / bound).max()
     assert (lse.double() - np.log(n)).abs().max() <= 2.0 ** -22 * np.log(n)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,group,page", FORMS)
+def test_key_lengths_of_any_size(dtype, D, group, page):
+    """1 / max(||row||, 1e-12) of rows whose squares overflow or vanish in a float, between ordinary ones.
+
+    Sum of D squares: D / 8 + 5 roundings of 2^-24, then a root, a quotient and (from 2^126 on) a denormal's.
+    """
+    sizes = [1.0, 1e18, 1e19, 3e19, 1e20, 1.0, 1e25, 1e31, 1e36, 3e37, 0.0, 1e-13, 1e-30, 1e19, 1.0, 1e-18, 2e20]
+    g = torch.Generator().manual_seed(83)
+    k = torch.randn(1, 2, len(sizes) + 6, D, generator=g).clamp(-4, 4)
+    k[:, :, :len(sizes)] *= torch.tensor(sizes)[:, None]
+    k[:, 0, -6:, 3] = torch.tensor([float("inf"), float("-inf"), float("nan"), 1e30, 2e38, 3.3e38])
+    k = k.to(dtype)
+    n = k.shape[2]
+    c = Cache(83, B=1, H=2, D=D, group=group, page=page, ctx=(n,), rows=(k, k.flip(3).contiguous()))
+    _, _, inv = lsh.lsh_cache_read(c.cache, c.table, c.ctx_len, n, D, **c.form)
+    want = co.oracle_key_inv(np64(k))
+    assert np.isnan(want).sum() == 1 and (want == 0).sum() == 2
+    assert np.allclose(np64(inv), want, rtol=(D / 8 + 8) * 2.0 ** -24, atol=2.0 ** -149, equal_nan=True)
+    assert _status() == 0
