@@ -70,6 +70,7 @@ constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kMaxEntries = 256;     // pages looked up at a time
 constexpr int kBlockTiles = 8;       // 128 tokens: what the work is dealt out in
 constexpr float kLazyMax = 8.f;
+constexpr float kPlainUnit = 0x1p-26f;  // of plain keys' scales: 2^-100 of them is still a normal number
 
 struct AttendArgs {
   const void* q;            // [B, H * G, T, D]
@@ -531,7 +532,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       self[nt] = other;
     }
     if (live && (a.causal || a.self_mask)) fast = min(fast, pos[nt]);
-    step[nt] = qstep[cc];
+    step[nt] = a.unit_keys ? qstep[cc] : qstep[cc] * (1.f / kPlainUnit);
 #pragma unroll
     for (int n = 0; n < NG; ++n) qsum[nt][n] = qs[cc * NG + n];
   }
@@ -593,12 +594,19 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
       float acc[NT][2], zero[NT][2];  // sum of s (codes . q) in steps of q, and of z (sum of q)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = zero[nt][0] = zero[nt][1] = 0.f;
+      // The key's length goes into s and z, which leaves them below 1 whatever the row's size; of plain keys s is taken
+      // in units that leave room for a sum of codes and queries, up to 2^36 (step has the factor back).
+      float ks[2] = {kPlainUnit, kPlainUnit}, kz[2] = {1.f, 1.f};
+      if (a.unit_keys) {
+        ks[0] = kz[0] = reinterpret_cast<const float*>(tb + F::kOffInv)[g];
+        ks[1] = kz[1] = reinterpret_cast<const float*>(tb + F::kOffInv)[g + 8];
+      }
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const uint32_t pw = kp[n * 16 + g + 8 * r];
-          const float sc = bf16_bits(pw), ze = __uint_as_float(pw & 0xffff0000u);
+          const float sc = bf16_bits(pw) * ks[r], ze = __uint_as_float(pw & 0xffff0000u) * kz[r];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             // at most 64 * 15 * 2^15; the third byte joins in float
@@ -609,19 +617,16 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
           }
         }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float fk = a.scale_log2;
-        if (a.unit_keys) fk *= reinterpret_cast<const float*>(tb + F::kOffInv)[g + 8 * r];
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float x = fmaf(acc[nt][r], step[nt], zero[nt][r]) * fk;
+          float x = fmaf(acc[nt][r], step[nt], zero[nt][r]) * a.scale_log2;
           if (MASKED) {
             const int key = first_mine + g + 8 * r;
             if (first_mine < 0 || key > last[nt] || (key == pos[nt] && self[nt])) x = -INFINITY;
           }
           s[f][nt][r] = x;
         }
-      }
     }
     // ---- the running maximum, moved only when a logit is 2^8 above it
     float top[NT];

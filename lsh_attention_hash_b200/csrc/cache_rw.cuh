@@ -303,8 +303,8 @@ struct WriteArgs {
 
 // 1 / length of a row whose squares overflow a float (it is longer than 1.8e19), from the row scaled by 2^-96; 0 for a
 // row with an infinity, NaN for one with a NaN.  One lane reads the row again: the common case pays a comparison (bf16
-// nothing that shows, fp32 217 -> 226 us for 8 heads x 262144 rows of 64, as its registers are full; the whole warp by a vote 222,
-// but bf16 5 % more).
+// nothing that shows, fp32 217 -> 226 us for 8 heads x 262144 rows of 64, as its registers are full; the whole warp by
+// a vote 222, but bf16 5 % more).
 template <typename T, int D>
 __device__ __noinline__ float long_row_inv(const T* row) {
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

@@ -9,7 +9,7 @@ import torch
 
 import lsh_attention_hash_b200 as lsh
 from oracle import cache_oracle as co
-from tests.test_gpu_cache import DEV, Cache, _status, np64
+from tests.test_gpu_cache import DEV, Cache, _check_attend, _status, np64
 
 pytestmark = pytest.mark.gpu
 
@@ -120,4 +120,23 @@ def test_key_lengths_of_any_size(dtype, D, group, page):
     want = co.oracle_key_inv(np64(k))
     assert np.isnan(want).sum() == 1 and (want == 0).sum() == 2
     assert np.allclose(np64(inv), want, rtol=(D / 8 + 8) * 2.0 ** -24, atol=2.0 ** -149, equal_nan=True)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G", [1, 2, 8])
+@pytest.mark.parametrize("unit_keys", [True, False])
+@pytest.mark.parametrize("size", [1e-35, 1e-25, 1e18, 1e20, 1e30, 1e33, 1e36])
+def test_keys_of_any_size(dtype, G, unit_keys, size):
+    """Keys near both ends of the range, plain ones with a scale that keeps their logits ordinary."""
+    g = torch.Generator().manual_seed(84)
+    k = (torch.randn(1, 2, 150, 64, generator=g).clamp(-4, 4) * 0.25 * size).to(dtype)
+    v = torch.randn(1, 2, 150, 64, generator=g).to(dtype)
+    c = Cache(84, dtype=dtype, B=1, H=2, D=64, group=32, page=32, ctx=(150,), rows=(k, v))
+    q = torch.randn(1, 2 * G, 1, 64, generator=g).clamp(-4, 4).to(dtype).to(DEV)
+    scale = 0.5 if unit_keys else min(0.5 / size, 1e37)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, unit_keys=unit_keys, scale=scale,
+                                    out_dtype=torch.float32, **c.form)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    _check_attend(c, q, out, lse, [1], unit_keys=unit_keys, scale=scale)
     assert _status() == 0
