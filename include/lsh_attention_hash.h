@@ -407,11 +407,13 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *
  * The products with the codes are exact integer sums of fixed-point numbers: a query in steps of
  * its largest entry / 8355711, a weight (softmax numerator times the value's scale) in steps of 2^-22 of
- * the power of two at or below the largest of its 64 keys' weights.  Everything else is fp32; keys
+ * the power of two at or below the largest of its 64 keys' weights, 2^-127 at the finest.  Everything else is
+ * fp32; keys
  * in any order give the same result only up to rounding, the same call the same bits.
  * A query row with an infinity or a NaN answers NaN.  Keys may reach 1e36 in size; of plain keys (unit_keys 0)
- * sum_d |q_d K_d|, before the scale, stays below 1e38.  Stored values may
- * reach 1e36 (beyond that a weight times a scale can overflow).
+ * sum_d |q_d K_d|, before the scale, stays below 1e38.  The
+ * size of the stored values times the number of a row's keys may reach 1e35 (beyond, the sum before its division by the
+ * weights' sum, which are up to 2^8, can overflow: infinities or NaN).
  * lse makes the result joinable with other key sets by lsh_combine_rounds, where one of
  * them has a key for the row.
  */

@@ -140,3 +140,60 @@ def test_keys_of_any_size(dtype, G, unit_keys, size):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     _check_attend(c, q, out, lse, [1], unit_keys=unit_keys, scale=scale)
     assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("size", [1.0, 1e-20, 1e-26, 1e-28, 1e-29, 4e-30])
+def test_values_of_any_smallness(dtype, size):
+    """Values down to the smallest scale (2^-100), one dominant key and many whose weights are small, in stages that
+    hold masked keys too.
+
+    As in test_weights_keep_the_precision_of_floats, with steps that end at 2^-127: n keys are then off by n * 15 * 2^-128.
+    """
+    n, T, D, group = 650, 8, 64, 32
+    g = torch.Generator().manual_seed(85)
+    k = torch.zeros(1, 1, n, D)
+    k[..., 0] = 1.0
+    k[:, :, 5, 0] = 40.0
+    k[:, :, 6:, 1] = torch.rand(1, 1, n - 6, generator=g) * 6
+    v = torch.randn(1, 1, n, D, generator=g) * size
+    c = Cache(85, B=1, H=1, D=D, group=group, page=64, ctx=(n,), rows=(k, v))
+    q = torch.zeros(1, 1, T, D, dtype=dtype)
+    q[..., 0], q[..., 1] = 1.5, -1.0
+    out, lse = lsh.lsh_cache_attend(q.to(DEV), c.cache, c.table, c.ctx_len, unit_keys=False, out_dtype=torch.float32,
+                                    **c.form)
+    K, V, inv = c.stored(0, 0)
+    _, _, zk = co.oracle_quantise(np64(k[0, 0]), group)
+    _, sv, zv = co.oracle_quantise(np64(v[0, 0]), group)
+    zK, zV, sV = (np.repeat(x, group, axis=1) for x in (zk, zv, sv))
+    for t in range(T):
+        x, pos = np64(q[0, 0, t]), n - T + t
+        want, wl, w, keys = co.oracle_cache_attend_row(x, K, V, inv, pos, n, None, 64, True, True, False, None)
+        code = np.abs(K - zK)
+        dz = (0.5 * np.abs(x).max() / 8355711 * code.sum(1) + 2.0 ** -20 * ((code + np.abs(zK)) @ np.abs(x))) / 8
+        rel = 2 * dz.max() + 2.0 ** -18
+        bound = n * 15 * (2.0 ** -23 * (w[:, None] * sV[keys]).max(0) + 2.0 ** -128)
+        bound = bound + rel * (w @ (np.abs(V - zV) + np.abs(zV))[keys])
+        err = np.abs(np64(out[0, 0, t]) - want)
+        assert (err <= bound).all(), (t, (err / bound).max(), err.max() / size)
+        assert abs(float(lse[0, 0, t]) - wl) <= rel + 2.0 ** -22 * abs(wl)
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [300, 5000])
+def test_values_of_any_size(dtype, n):
+    """Values of one sign whose sum over the keys is 1e35, with equal weights and with the largest logit last."""
+    g = torch.Generator().manual_seed(86)
+    v = (1 + torch.rand(1, 1, n, 64, generator=g)) * (0.5e35 / n)
+    k = torch.zeros(1, 1, n, 64)
+    k[..., 0] = torch.linspace(0.0, 5.0, n)
+    c = Cache(86, dtype=torch.float32, B=1, H=1, D=64, group=64, page=64, ctx=(n,), rows=(k, v))
+    for q0 in (0.0, 8.0):
+        q = torch.zeros(1, 1, 1, 64, dtype=dtype, device=DEV)
+        q[..., 0] = q0
+        out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, unit_keys=False, self_mask=False,
+                                        out_dtype=torch.float32, **c.form)
+        assert torch.isfinite(out).all()
+        _check_attend(c, q, out, lse, [1], unit_keys=False, self_mask=False)
+    assert _status() == 0
