@@ -67,9 +67,16 @@ __device__ __forceinline__ GroupParams group_params(float lo, float hi) {
   const float q = span * (1.f / 15.f);  // off by 3 units of its last place at most
   uint32_t b = __float_as_uint(q);
   if ((b & 0xffffu) - 0x7ffcu <= 8u) {  // the middle of two bf16 is that near: the exact quotient decides
-    const double d = (double)hi - (double)g.z;
+    const double h = (double)hi, z = (double)g.z, d = h - z;
+    // what d leaves out of hi - z (bf16: where it leaves something out, d is next to a number of 8 bits, and the middle,
+    // 15 times an odd one of 9 bits, is not)
+    double lost = 0.0;
+    if (sizeof(T) == 4) {
+      const double back = d - h;
+      lost = (h - (d - back)) + (-z - back);
+    }
     const double mid = 15.0 * (double)__uint_as_float((b & 0xffff0000u) | 0x8000u);
-    const bool up = d > mid || (d == mid && (b & 0x10000u));
+    const bool up = d > mid || (d == mid && (lost > 0.0 || (lost == 0.0 && (b & 0x10000u))));
     b = (b & 0xffff0000u) + (up ? 0x10000u : 0u);
   } else {
     b = (b + 0x8000u) & 0xffff0000u;

@@ -197,3 +197,68 @@ def test_values_of_any_size(dtype, n):
         assert torch.isfinite(out).all()
         _check_attend(c, q, out, lse, [1], unit_keys=False, self_mask=False)
     assert _status() == 0
+
+
+def _rational_stored(x):
+    """Stored values of one group in rational arithmetic (finite, no denormals)."""
+    x = [Fraction(float(t)) for t in x]
+
+    def bf16(f, nearest):  # the largest bf16 not above f, or the nearest (ties to even)
+        if f == 0:
+            return f
+        a, e = abs(f), 0
+        while a >= 2:
+            a, e = a / 2, e + 1
+        while a < 1:
+            a, e = a * 2, e - 1
+        step = Fraction(2) ** (e - 7)
+        n = f / step
+        low = n.numerator // n.denominator
+        r = n - low
+        return step * (low + (nearest and (r > Fraction(1, 2) or (r == Fraction(1, 2) and low % 2 == 1))))
+
+    z = bf16(min(x), False)
+    s = bf16((max(x) - z) / 15, True)
+    if s < Fraction(2) ** -100:
+        return [float(z)] * len(x)
+    out = []
+    for t in x:
+        q = (t - z) / s
+        low = q.numerator // q.denominator
+        r = q - low
+        c = min(15, low + (r > Fraction(1, 2) or (r == Fraction(1, 2) and low % 2 == 1)))
+        out.append(z + s * c)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantiser_next_to_every_border(dtype):
+    """Scales and codes whose quotient lies on a border or as near to it as the type allows, with zeros so small
+    that neither a float's nor a double's difference shows them; against rational arithmetic."""
+    g = np.random.default_rng(87)
+    rows = []
+    for i in range(400):
+        m = int(g.integers(128, 256))
+        e = float(2.0 ** g.integers(-20, 20))
+        z = [0.0, -2.0 ** -80, 2.0 ** -80, -3 * 2.0 ** -60, 2.0 ** -40, -1.0, 1.0, -200.0][i % 8]
+        s = m * e
+        top = 15 * (s + [0, 0.5 * e, e * 2.0 ** -7, -0.5 * e][(i // 8) % 4])  # on, half a step beside, near
+        x = z + (g.integers(0, 15, 32) + 0.5) * s
+        x = x.astype(np.float32)
+        for step in (-1.0, 1.0):
+            part = g.random(32) < 0.25
+            x[part] = np.nextafter(x[part], np.float32(step * 3e38))
+        x[0], x[1] = z, top if z else 3855.0 * e
+        rows.append(x)
+    x = torch.from_numpy(np.stack(rows).reshape(200, 64)).to(dtype)
+    n = x.shape[0]
+    c = Cache(87, dtype=dtype, B=1, H=1, D=64, group=32, page=16, ctx=(n,), rows=(x[None, None], x.flip(1)[None, None].contiguous()))
+    k, v, _ = lsh.lsh_cache_read(c.cache, c.table, c.ctx_len, n, 64, out_dtype=torch.float32, **c.form)
+    for got, src in ((k, x), (v, x.flip(1))):
+        for r in range(n):
+            want = []
+            for a in (0, 32):
+                want += _rational_stored(src[r, a:a + 32].double().tolist())
+            # one rounding of the rational value to float32 (float() of a Fraction is the nearest double; where that is
+            # halfway between two floats, it is the value itself)
+            assert got[0, 0, r].tolist() == [float(np.float32(float(t))) for t in want], r
