@@ -521,6 +521,8 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
     n_select, sel = 0, None
     if selected is not None:
         n_select = _rows4(selected, "selected")[3]
+        if n_select < 1:  # (an empty tensor's pointer is null, which would mean every page)
+            raise ValueError("selected must list at least one page for each row (-1 for none)")
         sel = _fit(selected, "selected", torch.int32, (B, H, T, n_select), dev)
     out_dtype = q.dtype if out_dtype is None else out_dtype
     if out_dtype not in _DT:

@@ -109,3 +109,15 @@ def test_a_refused_launch_is_reported_once(which):
     call()
     torch.cuda.synchronize()
     assert _status() == 0
+
+
+def test_an_empty_list_of_pages_is_refused():
+    """A list without places is not "every page"; a list of -1 answers as no key does."""
+    c = Cache(91, B=1, H=2, ctx=(40,))
+    q = c.rand(1, 2, 1, 128).to(DEV)
+    with pytest.raises(ValueError, match="at least one page"):
+        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, selected=torch.empty(1, 2, 1, 0, dtype=torch.int32, device=DEV),
+                             **c.form)
+    none = torch.full((1, 2, 1, 1), -1, dtype=torch.int32, device=DEV)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, selected=none, **c.form)
+    assert (out == 0).all() and torch.isneginf(lse).all() and _status() == 0
