@@ -378,13 +378,17 @@ def _need_cache(cache, D, page, group):
 
 
 def _need_pages(page_table, ctx_len, new_len, dev):
-    """(B, max_pages, the three pointers)."""
+    """(B, max_pages, the three pointers).
+
+    A tensor without elements has a null pointer, which the library takes for one left out: where a call
+    has rows and yet an empty table (or cache), it gets the lengths' pointer in its place, of which nothing is read.
+    """
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     shape = page_table.shape
     lengths = shape[:1]
-    return (shape[0], shape[1], _fit(page_table, "page_table", torch.int32, shape, dev),
-            _fit(ctx_len, "ctx_len", torch.int32, lengths, dev),
+    ctx = _fit(ctx_len, "ctx_len", torch.int32, lengths, dev)
+    return (shape[0], shape[1], _fit(page_table, "page_table", torch.int32, shape, dev) or ctx, ctx,
             None if new_len is None else _fit(new_len, "new_len", torch.int32, lengths, dev))
 
 
@@ -430,11 +434,13 @@ def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_
         if buckets is None or tags is None:
             raise ValueError("buckets and tags go together")
         n_rounds = _rows4(tags, "tags")[2]
-        tg = _fit(tags, "tags", torch.int16, (n_pages, H, n_rounds, page), dev)
+        tg = _fit(tags, "tags", torch.int16, (n_pages, H, n_rounds, page), dev) or (ctx if n_rounds else None)
         bk = _fit(buckets, "buckets", torch.int32, (B, H, n_rounds, T), dev)
-    _on_device(dev, device, lib.lsh_cache_write, "lsh_cache_write", k.data_ptr(), _fit(v, "v", k.dtype, shape, dev), dt,
-               B, H, T, D, bk, n_rounds, ctx, new, table, max_pages, page, group,
-               _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, tg)
+    vp, cp = _fit(v, "v", k.dtype, shape, dev), _fit(cache, "cache", torch.uint8, cache.shape, dev) or ctx
+    if B * H * T == 0:
+        return
+    _on_device(dev, device, lib.lsh_cache_write, "lsh_cache_write", k.data_ptr(), vp, dt, B, H, T, D, bk, n_rounds, ctx,
+               new, table, max_pages, page, group, cp, n_pages, tg)
 
 
 @_on_stream
@@ -455,8 +461,10 @@ def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_l
     k, kp = _new(k, "k", out_dtype, shape, cache)
     v, vp = _new(v, "v", out_dtype, shape, k)
     key_inv, ip = _new(key_inv, "key_inv", torch.float32, shape[:3], cache)
-    _on_device(dev, device, lib.lsh_cache_read, "lsh_cache_read", cache.data_ptr(), n_pages, B, H, T, D, ctx, new, table,
-               max_pages, page, group, kp, vp, _DT[out_dtype], ip)
+    if B * H * T == 0:
+        return k, v, key_inv
+    _on_device(dev, device, lib.lsh_cache_read, "lsh_cache_read", cache.data_ptr() or ctx, n_pages, B, H, T, D, ctx,
+               new, table, max_pages, page, group, kp, vp, _DT[out_dtype], ip)
     return k, v, key_inv
 
 
@@ -481,10 +489,12 @@ def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=
         raise ValueError("n_select must be at least 1")
     selected, sp = _new(selected, "selected", torch.int32, (B, H, T, n_select), tags)
     scores, cp = _new(scores, "scores", torch.int32, (B, H, T, max_pages), tags)
-    _on_device(dev, device, lib.lsh_cache_select, "lsh_cache_select",
-               _fit(tags, "tags", torch.int16, tags.shape, dev), n_pages,
-               _fit(q_buckets, "q_buckets", torch.int32, q_buckets.shape, dev), B, Hq, H, T, n_rounds, ctx, new, table,
-               max_pages, page, n_select, n_local, 2 if causal else 0, sp, cp)
+    tp = _fit(tags, "tags", torch.int16, tags.shape, dev) or ctx
+    qp = _fit(q_buckets, "q_buckets", torch.int32, q_buckets.shape, dev)
+    if B * H * T == 0:
+        return selected, scores
+    _on_device(dev, device, lib.lsh_cache_select, "lsh_cache_select", tp, n_pages, qp, B, Hq, H, T, n_rounds, ctx,
+               new, table, max_pages, page, n_select, n_local, 2 if causal else 0, sp, cp or sp)
     return selected, scores
 
 
@@ -529,6 +539,9 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
         raise ValueError(f"unsupported dtype {out_dtype}")
     out, op = _new(out, "out", out_dtype, shape, q)
     lse, lp = _new(lse, "lse", torch.float32, shape[:3], q)
+    cp = _fit(cache, "cache", torch.uint8, cache.shape, dev) or ctx
+    if B * Hq * T == 0:
+        return out, lse
     ws, nbytes = None, 0
     if workspace is None:
         nbytes = _attend_workspace(dt, B, Hq, H, T, D, max_pages, page, n_select, dev.index)
@@ -537,9 +550,9 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
             ws = workspace.data_ptr()
     else:
         ws, nbytes = _fit(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel()
-    _on_device(dev, device, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D,
-               _fit(cache, "cache", torch.uint8, cache.shape, dev), n_pages, ctx, new, table, max_pages, page, group, sel,
-               n_select, (1 if self_mask else 0) | (2 if causal else 0), 1 if unit_keys else 0,
+    _on_device(dev, device, lib.lsh_cache_attend, "lsh_cache_attend", q.data_ptr(), dt, B, Hq, H, T, D, cp, n_pages, ctx,
+               new, table, max_pages, page, group, sel, n_select, (1 if self_mask else 0) | (2 if causal else 0),
+               1 if unit_keys else 0,
                0.0 if scale is None else float(scale), op, _DT[out_dtype], lp, ws, nbytes)
     return out, lse
 
@@ -606,7 +619,10 @@ def lsh_attention_decode(qk, v, R, n_buckets, cache, tags, page_table, ctx_len, 
                                         scale=scale, bufs=bufs, check=check)
     buckets = None
     if tags is not None:
-        buckets, _ = lsh_hash(qk, R, n_buckets, buckets=b.get("buckets"), with_near_tie=False)
+        if qk.numel():
+            buckets, _ = lsh_hash(qk, R, n_buckets, buckets=b.get("buckets"), with_near_tie=False)
+        else:
+            buckets = qk.new_empty((*qk.shape[:2], R.shape[0], qk.shape[2]), dtype=torch.int32)
     lsh_cache_write(qk, v, cache, page_table, ctx_len, page=page, group=group, new_len=new_len, buckets=buckets,
                     tags=tags)
     selected = None

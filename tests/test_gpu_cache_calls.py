@@ -121,3 +121,54 @@ def test_an_empty_list_of_pages_is_refused():
     none = torch.full((1, 2, 1, 1), -1, dtype=torch.int32, device=DEV)
     out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, selected=none, **c.form)
     assert (out == 0).all() and torch.isneginf(lse).all() and _status() == 0
+
+
+def _empty(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device=DEV)
+
+
+@pytest.mark.parametrize("B,H,T", [(2, 2, 0), (0, 2, 3), (2, 0, 3), (0, 0, 0)])
+def test_calls_without_rows(B, H, T):
+    """No rows: empty answers of the right shapes, and nothing is written."""
+    cache, tags = lsh.alloc_cache(4, H, 128, n_rounds=3, device=DEV)
+    cache.fill_(7)
+    tags.fill_(7)
+    table, ctx = torch.zeros(B, 2, dtype=torch.int32, device=DEV), torch.full((B,), 5, dtype=torch.int32, device=DEV)
+    rows, bk = _empty(B, H, T, 128), _empty(B, H, 3, T, dtype=torch.int32)
+    lsh.lsh_cache_write(rows, rows, cache, table, ctx, buckets=bk, tags=tags, new_len=ctx)
+    k, v, inv = lsh.lsh_cache_read(cache, table, ctx, T, 128)
+    assert k.shape == v.shape == (B, H, T, 128) and inv.shape == (B, H, T)
+    sel, scores = lsh.lsh_cache_select(tags, bk, table, ctx, 2)
+    assert sel.shape == (B, H, T, 2) and scores.shape == (B, H, T, 2)
+    for s in (None, sel):
+        out, lse = lsh.lsh_cache_attend(rows, cache, table, ctx, selected=s)
+        assert out.shape == rows.shape and lse.shape == (B, H, T)
+    R = torch.randn(3, 128, 8, device=DEV).bfloat16()
+    for n_select in (0, 2):
+        out, lse = lsh.lsh_attention_decode(rows, rows, R, 16, cache, tags, table, ctx, n_select=n_select, check=True)
+        assert out.shape == rows.shape and lse.shape == (B, H, T)
+    assert (cache == 7).all() and (tags == 7).all() and _status() == 0
+
+
+@pytest.mark.parametrize("n_pages,max_pages", [(4, 0), (0, 0), (0, 2)])
+def test_calls_without_pages(n_pages, max_pages):
+    """Sequences without a token over tables, or a cache, of no pages: rows are padding."""
+    cache, tags = lsh.alloc_cache(n_pages, 2, 64, n_rounds=2, device=DEV)
+    cache.fill_(7)
+    table, ctx = torch.full((2, max_pages), -1, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    rows, bk = torch.randn(2, 2, 3, 64, device=DEV).bfloat16(), torch.zeros(2, 2, 2, 3, dtype=torch.int32, device=DEV)
+    lsh.lsh_cache_write(rows, rows, cache, table, ctx, buckets=bk, tags=tags)
+    k, v, inv = lsh.lsh_cache_read(cache, table, ctx, 3, 64)
+    assert (k == 0).all() and (v == 0).all() and (inv == 0).all()
+    sel, scores = lsh.lsh_cache_select(tags, bk, table, ctx, 2)
+    assert (sel == -1).all() and scores.shape == (2, 2, 3, max_pages) and (scores == -1).all()
+    for s in (None, sel):
+        out, lse = lsh.lsh_cache_attend(rows, cache, table, ctx, selected=s)
+        assert (out == 0).all() and torch.isneginf(lse).all()
+    out, lse = lsh.lsh_attention_decode(rows, rows, torch.randn(2, 64, 8, device=DEV).bfloat16(), 16, cache, tags, table,
+                                        ctx, n_select=1, check=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    assert (cache == 7).all() and _status() == 0
+    # tokens that no table has room for, or whose pages the cache lacks, are the caller's error
+    out, lse = lsh.lsh_cache_attend(rows, cache, table, ctx + 3)
+    assert (out == 0).all() and torch.isneginf(lse).all() and _status() == 1
