@@ -377,8 +377,19 @@ def _need_cache(cache, D, page, group):
     return shape[0], shape[1]
 
 
-def _need_pages(page_table, ctx_len, new_len, dev):
-    """(B, max_pages, the three pointers).
+def _ints(t, name, shape, dev, keep):
+    """The pointer of small int32 data: a copy's where a slice (``ctx_len[1:]``, say) starts between 16-byte
+    boundaries, which the library asks of every pointer.  ``keep`` holds the copy until the call is made."""
+    p = _fit(t, name, torch.int32, shape, dev)
+    if p & 15:
+        t = t.clone()
+        keep.append(t)
+        p = t.data_ptr()
+    return p
+
+
+def _need_pages(page_table, ctx_len, new_len, dev, keep):
+    """(B, max_pages, the three pointers); what has to live until the call goes into ``keep``.
 
     A tensor without elements has a null pointer, which the library takes for one left out: where a call
     has rows and yet an empty table (or cache), it gets the lengths' pointer in its place, of which nothing is read.
@@ -387,9 +398,9 @@ def _need_pages(page_table, ctx_len, new_len, dev):
         raise ValueError("page_table must be [B, max_pages]")
     shape = page_table.shape
     lengths = shape[:1]
-    ctx = _fit(ctx_len, "ctx_len", torch.int32, lengths, dev)
-    return (shape[0], shape[1], _fit(page_table, "page_table", torch.int32, shape, dev) or ctx, ctx,
-            None if new_len is None else _fit(new_len, "new_len", torch.int32, lengths, dev))
+    ctx = _ints(ctx_len, "ctx_len", lengths, dev, keep)
+    return (shape[0], shape[1], _ints(page_table, "page_table", shape, dev, keep) or ctx, ctx,
+            None if new_len is None else _ints(new_len, "new_len", lengths, dev, keep))
 
 
 def _new(t, name, dtype, shape, like):
@@ -426,7 +437,7 @@ def lsh_cache_write(k, v, cache, page_table, ctx_len, *, page=64, group=64, new_
     n_pages, Hc = _need_cache(cache, D, page, group)
     if Hc != H:
         raise ValueError(f"cache has {Hc} heads, k {H}")
-    Bt, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
+    Bt, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev, keep := [])
     if Bt != B:
         raise ValueError(f"page_table has {Bt} sequences, k {B}")
     n_rounds, bk, tg = 0, None, None
@@ -454,7 +465,7 @@ def lsh_cache_read(cache, page_table, ctx_len, T, D, *, page=64, group=64, new_l
     lib = load_library()
     n_pages, H = _need_cache(cache, D, page, group)
     dev = cache.device
-    B, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
+    B, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev, keep := [])
     if out_dtype not in _DT:
         raise ValueError(f"unsupported dtype {out_dtype}")
     shape = (B, H, T, D)
@@ -481,7 +492,7 @@ def lsh_cache_select(tags, q_buckets, page_table, ctx_len, n_select, *, new_len=
     lib = load_library()
     n_pages, H, n_rounds, page = _rows4(tags, "tags")
     dev = tags.device
-    B, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
+    B, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev, keep := [])
     Bq, Hq, Rq, T = _rows4(q_buckets, "q_buckets")
     if Bq != B or Rq != n_rounds:
         raise ValueError(f"q_buckets must be [{B}, Hq, {n_rounds}, T]")
@@ -525,7 +536,7 @@ def lsh_cache_attend(q, cache, page_table, ctx_len, *, page=64, group=64, new_le
     dt = _dt(q)
     dev = q.device
     n_pages, H = _need_cache(cache, D, page, group)
-    Bt, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev)
+    Bt, max_pages, table, ctx, new = _need_pages(page_table, ctx_len, new_len, dev, keep := [])
     if Bt != B:
         raise ValueError(f"page_table has {Bt} sequences, q {B}")
     n_select, sel = 0, None

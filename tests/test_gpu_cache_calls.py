@@ -172,3 +172,44 @@ def test_calls_without_pages(n_pages, max_pages):
     # tokens that no table has room for, or whose pages the cache lacks, are the caller's error
     out, lse = lsh.lsh_cache_attend(rows, cache, table, ctx + 3)
     assert (out == 0).all() and torch.isneginf(lse).all() and _status() == 1
+
+
+def test_slices_of_lengths_and_tables():
+    """Lengths and tables that start between 16-byte boundaries, as slices of a batch do, in eager calls and in a
+    captured one that follows their contents."""
+    c = Cache(92, B=3, H=2, ctx=(50, 90, 130), n_rounds=2)
+    wide = torch.full((4, 5), -1, dtype=torch.int32, device=DEV)  # odd width: row 1 starts 20 bytes in
+    wide[1:, :c.max_pages] = c.table
+    ctx = torch.cat([torch.zeros(1, dtype=torch.int32, device=DEV), c.ctx_len])
+    new = torch.tensor([0, 2, 1, 0], dtype=torch.int32, device=DEV)
+    assert wide[1:].data_ptr() % 16 and ctx[1:].data_ptr() % 16
+    k, v = c.rand(3, 2, 2, 128).to(DEV), c.rand(3, 2, 2, 128).to(DEV)
+    bk = torch.randint(0, 16, (3, 2, 2, 2), generator=c.g, dtype=torch.int32).to(DEV)
+
+    def step(cache, tags, table, ctx, new):
+        lsh.lsh_cache_write(k, v, cache, table, ctx, new_len=new, buckets=bk, tags=tags, **c.form)
+        got = list(lsh.lsh_cache_read(cache, table, ctx, 2, 128, new_len=new, **c.form))
+        got += lsh.lsh_cache_select(tags, bk, table, ctx, 2, new_len=new)  # got[3]: the selection
+        got += lsh.lsh_cache_attend(k, cache, table, ctx, new_len=new, selected=got[3], **c.form)
+        got += lsh.lsh_cache_attend(k, cache, table, ctx, new_len=new, **c.form)
+        return got + [cache, tags]
+
+    def same(a, b):
+        return all(torch.equal(x, y) for x, y in zip(a, b))
+
+    plain = lambda: step(c.cache.clone(), c.tags.clone(), wide[1:].clone(), ctx[1:].clone(), new[1:].clone())  # noqa: E731
+    assert same(step(c.cache.clone(), c.tags.clone(), wide[1:], ctx[1:], new[1:]), plain())
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    cache, tags = c.cache.clone(), c.tags.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(cache, tags, wide[1:], ctx[1:], new[1:])
+    for i in range(3):
+        ctx[1:] -= 1
+        new[1:] = torch.tensor([1, 2 - i, i], dtype=torch.int32)
+        cache.copy_(c.cache)
+        tags.copy_(c.tags)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, plain())
+    assert _status() == 0
