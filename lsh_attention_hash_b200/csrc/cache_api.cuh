@@ -19,6 +19,9 @@ inline lsh_status check_cache_form(int H, int D, int page, int group, int n_page
   return LSH_OK;
 }
 
+// Whether a product of sizes (not negative, so at most 2^124) is below 2^31, the reach of rows and columns.
+inline bool fits_31_bits(int a, int b, int c, int d = 1) { return (__int128)a * b * c * d < ((__int128)1 << 31); }
+
 inline int log2_of(int p) {
   int l = 0;
   while ((1 << l) < p) ++l;
@@ -163,7 +166,7 @@ lsh_status lsh_cache_write(const void* k, const void* v, int dtype, int B, int H
   if (!valid_dtype(dtype)) return LSH_ERR_DTYPE;
   const lsh_status st = check_cache_form(H, D, page, group, n_pages, B, max_pages);
   if (st != LSH_OK) return st;
-  if (T < 0 || (long long)B * H * T >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if (T < 0 || !fits_31_bits(B, H, T)) return LSH_ERR_SHAPE;
   if ((buckets == nullptr) != (tags == nullptr)) return LSH_ERR_INVALID_ARG;
   if (tags && (n_rounds < 1 || n_rounds > 64)) return LSH_ERR_SHAPE;
   if (!k || !v || !ctx_len || !page_table || !cache) return LSH_ERR_INVALID_ARG;
@@ -201,7 +204,7 @@ lsh_status lsh_cache_read(const void* cache, int n_pages, int B, int H, int T, i
   if (!valid_dtype(out_dtype)) return LSH_ERR_DTYPE;
   const lsh_status st = check_cache_form(H, D, page, group, n_pages, B, max_pages);
   if (st != LSH_OK) return st;
-  if (T < 0 || (long long)B * H * T >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if (T < 0 || !fits_31_bits(B, H, T)) return LSH_ERR_SHAPE;
   if (!k || !v || !ctx_len || !page_table || !cache) return LSH_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(ctx_len) || !aligned16(page_table) || !aligned16(cache) ||
       (new_len && !aligned16(new_len)) || (key_inv && !aligned16(key_inv)))
@@ -237,8 +240,8 @@ lsh_status lsh_cache_select(const uint16_t* tags, int n_pages, const int32_t* q_
   if (T < 0 || Hq < 0 || (H == 0 ? Hq != 0 : (Hq % H != 0 || Hq == 0))) return LSH_ERR_SHAPE;
   if (n_rounds < 1 || n_rounds > 64 || n_select < 1 || n_local < 0 || n_local > n_select) return LSH_ERR_SHAPE;
   if ((long long)n_select * page > (1ll << 30)) return LSH_ERR_SHAPE;
-  if ((long long)B * H * T * std::max(1, n_select) >= (1ll << 31) ||
-      (long long)B * H * T * std::max(1, max_pages) >= (1ll << 31) || (long long)B * Hq * n_rounds * T >= (1ll << 31))
+  if (!fits_31_bits(B, H, T, n_select) || !fits_31_bits(B, H, T, std::max(1, max_pages)) ||
+      !fits_31_bits(B, Hq, n_rounds, T))
     return LSH_ERR_SHAPE;
   if (mask & ~LSH_MASK_CAUSAL) return LSH_ERR_INVALID_ARG;
   if (!tags || !q_buckets || !ctx_len || !page_table || !selected || !scores) return LSH_ERR_INVALID_ARG;
@@ -300,6 +303,8 @@ size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H, int T, 
                                         int n_select) {
   if (!valid_dtype(dtype) || check_cache_form(H, D, page, 32, 1, B, max_pages) != LSH_OK) return 0;
   if (H <= 0 || Hq <= 0 || Hq % H != 0 || T <= 0 || B <= 0 || n_select < 0) return 0;
+  if (!fits_31_bits(B, Hq, T) || !fits_31_bits(B, H, T, std::max(1, n_select))) return 0;
+  if ((long long)n_select * page > (1ll << 30)) return 0;
   return attend_plan_bytes(attend_plan(B, H, Hq / H, T, D, max_pages, page, n_select), D);
 }
 
@@ -312,10 +317,9 @@ lsh_status lsh_cache_attend(const void* q, int dtype, int B, int Hq, int H, int 
   const lsh_status st = check_cache_form(H, D, page, group, n_pages, B, max_pages);
   if (st != LSH_OK) return st;
   if (T < 0 || Hq < 0 || (H == 0 ? Hq != 0 : (Hq % H != 0 || Hq == 0))) return LSH_ERR_SHAPE;
-  if ((long long)B * Hq * T >= (1ll << 31)) return LSH_ERR_SHAPE;
+  if (!fits_31_bits(B, Hq, T)) return LSH_ERR_SHAPE;
   if (selected ? n_select < 1 : n_select != 0) return LSH_ERR_INVALID_ARG;
-  if ((long long)n_select * page > (1ll << 30) || (long long)B * H * T * std::max(1, n_select) >= (1ll << 31))
-    return LSH_ERR_SHAPE;
+  if ((long long)n_select * page > (1ll << 30) || !fits_31_bits(B, H, T, std::max(1, n_select))) return LSH_ERR_SHAPE;
   if (mask & ~(LSH_MASK_SELF | LSH_MASK_CAUSAL)) return LSH_ERR_INVALID_ARG;
   if (unit_keys != 0 && unit_keys != 1) return LSH_ERR_INVALID_ARG;
   if (!q || !cache || !ctx_len || !page_table || !out || !lse) return LSH_ERR_INVALID_ARG;
