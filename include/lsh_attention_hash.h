@@ -302,16 +302,16 @@ LSH_API lsh_status lsh_chunk_attend_backward(const void* qk, const void* v, int 
  * (largest - z) / 15; c = min(15, nearest integer to (x - z) / s, ties to even).  The
  * quotients are the real numbers', so equal rows are stored equally by every kernel.
  * A group whose s would be below 2^-100 is stored as z; a group that holds an infinity or a
- * NaN, or whose range overflows a float, reads back as NaN.  Each K row also keeps
- * 1 / max(||row||, 1e-12) of the row as it came, in fp32.  At D = 128 and group = 64 a
- * token takes 148 bytes per head.
+ * NaN, whose range overflows a float or whose smallest value lies below every bf16, reads back
+ * as NaN.  Each K row also keeps 1 / max(||row||, 1e-12) of the row as it came, in fp32 (0 with an
+ * infinity, NaN with a NaN).  At D = 128 and group = 64 a token takes 148 bytes per head.
  *
  * Positions: ctx_len [B] int32 counts the tokens of each sequence in the cache, this
  * call's among them.  Of the T rows of a call the first new_len[b] belong to sequence b
  * (new_len null: all T) and are its last tokens: row i is position ctx_len[b] -
  * new_len[b] + i.  Rows at or behind new_len[b], and rows whose position would be
- * negative, are padding (a new_len above T counts as T).  All three arrays are read on the device, so a captured graph
- * replays with their current contents.
+ * negative, are padding (a new_len above T counts as T).  All three arrays are read on the
+ * device, so a captured graph replays with their current contents.
  *
  * Caller errors that only the device can see are recorded as LSH_ERR_INVALID_ARG in the
  * device status word, and no access leaves a buffer: a ctx_len outside
@@ -407,13 +407,15 @@ LSH_API size_t lsh_cache_attend_workspace_bytes(int dtype, int B, int Hq, int H,
  *
  * The products with the codes are exact integer sums of fixed-point numbers: a query in steps of
  * its largest entry / 8355711, a weight (softmax numerator times the value's scale) in steps of 2^-22 of
- * the power of two at or below the largest of its 64 keys' weights, 2^-127 at the finest.  Everything else is
- * fp32; keys
- * in any order give the same result only up to rounding, the same call the same bits.
- * A query row with an infinity or a NaN answers NaN.  Keys may reach 1e36 in size; of plain keys (unit_keys 0)
- * sum_d |q_d K_d|, before the scale, stays below 1e38.  The
- * size of the stored values times the number of a row's keys may reach 1e35 (beyond, the sum before its division by the
- * weights' sum, which are up to 2^8, can overflow: infinities or NaN).
+ * the power of two at or below the largest of its 64 keys' weights, 2^-127 at the finest.  Everything
+ * else is fp32; keys in any order give the same result only up to rounding, the same call the same bits.
+ *
+ * Range.  A query row with an infinity or a NaN answers NaN; its largest entry lies between 1e-30 and
+ * 1e36 (below, its entries count with fewer digits).  Keys may reach 1e36 in size; of plain keys
+ * (unit_keys 0) sum_d |q_d K_d|, before the scale, stays below 1e38.  The size of the stored values times
+ * the number of a row's keys may reach 1e35 (beyond, the sum before its division by the weights' sum,
+ * which are up to 2^8, can overflow: infinities or NaN).
+ *
  * lse makes the result joinable with other key sets by lsh_combine_rounds, where one of
  * them has a key for the row.
  */

@@ -45,12 +45,13 @@
 // it, whatever the lengths are, so one wave of CTAs ends together.  An item inside one CTA is
 // written out there; the pieces of any other go to the workspace (a CTA has two at most: its
 // first and its last) and the join adds them up in order.  Where no item has more than 1024 keys,
-// each has a CTA to itself and there is nothing to join (8 heads of 1021 keys: 9 us on the device
-// either way, but a launch and a workspace less: 21 us a call with two kernels, 16 us with one).
+// each has a CTA to itself and there is nothing to join (8 heads of 1021 keys: 9.0 us on the device and
+// 17.5 us a call; with two kernels 8.3 us, but another launch and a workspace, 21 to 23 us a call).
 //
-// Measured, one new token, bf16: 8 x 8 heads x 65536 keys of 128 (621 MB) 105 us, 5.9 TB/s, 90 % of the
-// measured copy rate; 8 heads x 1 M keys of 64 (638 MB) 113 us, 5.6 TB/s, 86 %.  Four queries a cached head 110 us, 16 queries 264 us: there
-// the integer products and the unpacking (150 instructions a tile for one query) bind.
+// Measured on the device, one new token, bf16: 8 x 8 heads x 65536 keys of 128 (621 MB) 103 us, 6.0 TB/s, 92 %
+// of the measured copy rate; 8 heads x 1 M keys of 64 (638 MB) 104 us, 6.1 TB/s, 93 %.  Queries a cached head of
+// the former: 2 107 us, 4 114 us, 8 161 us, 16 294 us: from 4 on
+// the integer products and the unpacking (198 instructions a tile for one query, set-up and join included) bind.
 // The ring is two stages of 64 tokens a warp and 8 warps an SM at D 128: one stage and 16 warps took as long
 // there and 11 % more at D 64; three stages leave one CTA an SM (42 % more).
 #pragma once
@@ -719,7 +720,7 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
         }
 #pragma unroll
         for (int f = 0; f < SF; ++f) {
-          uint32_t x[NT][2];  // the number in the low bits of a float's mantissa (2^23 itself: as 0x4B800000, the same bytes)
+          uint32_t x[NT][2];  // the number in the low bits of a float's mantissa (2^23 itself, as 0x4B800000, too)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -732,8 +733,10 @@ cache_attend_kernel(const __grid_constant__ AttendArgs a) {
             pb[f][u][nt] = column(__byte_perm(x[nt][0], 0u, 0x4142), __byte_perm(x[nt][1], 0u, 0x4142));
 #pragma unroll
           for (int nt = 0; nt < NT; nt += 2) {
-            const uint32_t y0 = nt + 1 < NT ? x[nt + (nt + 1 < NT)][0] : 0u, y1 = nt + 1 < NT ? x[nt + (nt + 1 < NT)][1] : 0u;
-            pb[f][u][NT + nt / 2] = column(__byte_perm(x[nt][0], y0, 0x4400), __byte_perm(x[nt][1], y1, 0x4400));
+            const bool pair = nt + 1 < NT;
+            const uint32_t(&y)[2] = x[nt + pair];
+            pb[f][u][NT + nt / 2] = column(__byte_perm(x[nt][0], pair ? y[0] : 0u, 0x4400),
+                                           __byte_perm(x[nt][1], pair ? y[1] : 0u, 0x4400));
           }
         }
       }

@@ -14,9 +14,10 @@
 //   V params  the same
 //   K inv     16 floats: 1 / max(||row||, 1e-12)
 //
-// Both code layouts are what the lanes of a 16x8x16 matrix instruction hold:
-// lane 4g + t takes D/8 consecutive bytes of K row g, whose masked 16-bit pairs
-// are its A fragments, and D/8 consecutive bytes of V's token pair t.  The chunk
+// Both code layouts are what the lanes of a 16 x 8 x 32 product of 8-bit integers hold:
+// lane 4g + t takes D/8 consecutive bytes of K row g, of which a word's low nibbles and its
+// high nibbles are two registers of its A fragment, and D/8 consecutive bytes of V's token
+// pair t, whose bytes are dealt out to fragments by dims.  The chunk
 // XOR keeps the latter free of shared-memory bank conflicts.
 #pragma once
 

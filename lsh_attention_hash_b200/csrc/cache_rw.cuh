@@ -16,9 +16,9 @@
 // before they are bound by memory, so a code costs few: the three-input minimum and maximum of
 // sm_100, the integer taken from a float's mantissa, packing by multiply-add.
 //
-// Measured, 8 x 8 heads x 16384 rows: D 128 bf16 writing 196 us (3.5 TB/s: 610 instructions a warp for its
-// 1024 values bind it), reading 109 us (6.3 TB/s, 96 % of the measured copy rate); 8 heads x 262144 rows of 64 in
-// fp32: writing 226 us (5.5 TB/s), reading 191 us (6.5 TB/s).
+// Measured, 8 x 8 heads x 16384 rows: D 128 bf16 writing 198 us (3.5 TB/s: 630 instructions a warp for its
+// 1024 values bind it, three quarters of the issue slots), reading 111 us (6.25 TB/s, 95 % of the measured copy
+// rate); 8 heads x 262144 rows of 64 in fp32: writing 226 us (5.5 TB/s), reading 191 us (6.5 TB/s).
 #pragma once
 
 #include "cache_common.cuh"
@@ -68,8 +68,8 @@ __device__ __forceinline__ GroupParams group_params(float lo, float hi) {
   uint32_t b = __float_as_uint(q);
   if ((b & 0xffffu) - 0x7ffcu <= 8u) {  // the middle of two bf16 is that near: the exact quotient decides
     const double h = (double)hi, z = (double)g.z, d = h - z;
-    // what d leaves out of hi - z (bf16: where it leaves something out, d is next to a number of 8 bits, and the middle,
-    // 15 times an odd one of 9 bits, is not)
+    // what d leaves out of hi - z (bf16: where it leaves something out, d is next to a number of 8 bits, and the
+    // middle, 15 times an odd one of 9 bits, is not)
     double lost = 0.0;
     if (sizeof(T) == 4) {
       const double back = d - h;

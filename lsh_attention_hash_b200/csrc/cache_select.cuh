@@ -13,8 +13,11 @@
 // in, then one pass that writes the chosen pages in ascending order, of equal scores those of the
 // lowest pages.
 //
-// Measured, inputs not in L2: 64 heads x 65536 tokens, 8 rounds (67 MB of tags, floor 10 us) 20 us for both
-// kernels; 8 heads x 1 M tokens, 4 rounds (67 MB) 27 us.
+// Measured on the device, inputs not in L2: 64 heads x 65536 tokens, 8 rounds (67 MB of tags, floor 10 us) 20 us for
+// both kernels; 8 heads x 1 M tokens, 4 rounds (67 MB) 26 us.  What does not fit the batches of pages (several query
+// heads, other numbers of tags) takes the general loop, a page at a time: 64 heads x 65536 tokens, 6 rounds 30 us
+// (50 MB), 2 rounds 18 us (17 MB), 8 rounds with 4 query heads a head 49 us; 5 rows in the batches, which read the tags
+// for each, 53 us.
 #pragma once
 
 #include "cache_common.cuh"

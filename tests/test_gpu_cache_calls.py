@@ -6,13 +6,11 @@ import subprocess
 import sys
 import threading
 
-import numpy as np
 import pytest
 import torch
 
 import lsh_attention_hash_b200 as lsh
-from oracle import cache_oracle as co
-from tests.test_gpu_cache import DEV, Cache, _status, np64
+from tests.test_gpu_cache import DEV, Cache, _status
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -116,8 +114,8 @@ def test_an_empty_list_of_pages_is_refused():
     c = Cache(91, B=1, H=2, ctx=(40,))
     q = c.rand(1, 2, 1, 128).to(DEV)
     with pytest.raises(ValueError, match="at least one page"):
-        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, selected=torch.empty(1, 2, 1, 0, dtype=torch.int32, device=DEV),
-                             **c.form)
+        lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len,
+                             selected=torch.empty(1, 2, 1, 0, dtype=torch.int32, device=DEV), **c.form)
     none = torch.full((1, 2, 1, 1), -1, dtype=torch.int32, device=DEV)
     out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, selected=none, **c.form)
     assert (out == 0).all() and torch.isneginf(lse).all() and _status() == 0
@@ -155,7 +153,8 @@ def test_calls_without_pages(n_pages, max_pages):
     """Sequences without a token over tables, or a cache, of no pages: rows are padding."""
     cache, tags = lsh.alloc_cache(n_pages, 2, 64, n_rounds=2, device=DEV)
     cache.fill_(7)
-    table, ctx = torch.full((2, max_pages), -1, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    table = torch.full((2, max_pages), -1, dtype=torch.int32, device=DEV)
+    ctx = torch.zeros(2, dtype=torch.int32, device=DEV)
     rows, bk = torch.randn(2, 2, 3, 64, device=DEV).bfloat16(), torch.zeros(2, 2, 2, 3, dtype=torch.int32, device=DEV)
     lsh.lsh_cache_write(rows, rows, cache, table, ctx, buckets=bk, tags=tags)
     k, v, inv = lsh.lsh_cache_read(cache, table, ctx, 3, 64)
@@ -165,8 +164,8 @@ def test_calls_without_pages(n_pages, max_pages):
     for s in (None, sel):
         out, lse = lsh.lsh_cache_attend(rows, cache, table, ctx, selected=s)
         assert (out == 0).all() and torch.isneginf(lse).all()
-    out, lse = lsh.lsh_attention_decode(rows, rows, torch.randn(2, 64, 8, device=DEV).bfloat16(), 16, cache, tags, table,
-                                        ctx, n_select=1, check=True)
+    R = torch.randn(2, 64, 8, device=DEV).bfloat16()
+    out, lse = lsh.lsh_attention_decode(rows, rows, R, 16, cache, tags, table, ctx, n_select=1, check=True)
     assert (out == 0).all() and torch.isneginf(lse).all()
     assert (cache == 7).all() and _status() == 0
     # tokens that no table has room for, or whose pages the cache lacks, are the caller's error
@@ -197,7 +196,9 @@ def test_slices_of_lengths_and_tables():
     def same(a, b):
         return all(torch.equal(x, y) for x, y in zip(a, b))
 
-    plain = lambda: step(c.cache.clone(), c.tags.clone(), wide[1:].clone(), ctx[1:].clone(), new[1:].clone())  # noqa: E731
+    def plain():
+        return step(c.cache.clone(), c.tags.clone(), wide[1:].clone(), ctx[1:].clone(), new[1:].clone())
+
     assert same(step(c.cache.clone(), c.tags.clone(), wide[1:], ctx[1:], new[1:]), plain())
     s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
     cache, tags = c.cache.clone(), c.tags.clone()

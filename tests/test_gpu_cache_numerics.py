@@ -65,7 +65,8 @@ def test_weights_keep_the_precision_of_floats(dtype, D, group, page, G, wide):
         x = np64(q[0, hq, 0])
         want, wl, w, _ = co.oracle_cache_attend_row(x, K, V, inv, n - 1, n, None, page, False, True, False, None)
         code = np.abs(K - zK)
-        dz = (0.5 * np.abs(x).max() / 8355711 * code.sum(1) + 2.0 ** -20 * ((code + np.abs(zK)) @ np.abs(x))) / np.sqrt(D)
+        dz = 0.5 * np.abs(x).max() / 8355711 * code.sum(1) + 2.0 ** -20 * ((code + np.abs(zK)) @ np.abs(x))
+        dz = dz / np.sqrt(D)
         z = K @ x / np.sqrt(D)
         rel = 2 * dz.max() + np.abs(z - z.max()).max() * 2.0 ** -23 + 2.0 ** -21 + n * 2.0 ** -23
         bound = n * 15 * 2.0 ** -23 * (w[:, None] * sV).max(0) + rel * (w @ (np.abs(V - zV) + np.abs(zV)))
@@ -148,7 +149,8 @@ def test_values_of_any_smallness(dtype, size):
     """Values down to the smallest scale (2^-100), one dominant key and many whose weights are small, in stages that
     hold masked keys too.
 
-    As in test_weights_keep_the_precision_of_floats, with steps that end at 2^-127: n keys are then off by n * 15 * 2^-128.
+    As in test_weights_keep_the_precision_of_floats, with steps that end at 2^-127: n keys are then off by
+    n * 15 * 2^-128.
     """
     n, T, D, group = 650, 8, 64, 32
     g = torch.Generator().manual_seed(85)
@@ -252,7 +254,8 @@ def test_quantiser_next_to_every_border(dtype):
         rows.append(x)
     x = torch.from_numpy(np.stack(rows).reshape(200, 64)).to(dtype)
     n = x.shape[0]
-    c = Cache(87, dtype=dtype, B=1, H=1, D=64, group=32, page=16, ctx=(n,), rows=(x[None, None], x.flip(1)[None, None].contiguous()))
+    c = Cache(87, dtype=dtype, B=1, H=1, D=64, group=32, page=16, ctx=(n,),
+              rows=(x[None, None], x.flip(1)[None, None].contiguous()))
     k, v, _ = lsh.lsh_cache_read(c.cache, c.table, c.ctx_len, n, 64, out_dtype=torch.float32, **c.form)
     for got, src in ((k, x), (v, x.flip(1))):
         for r in range(n):
@@ -262,3 +265,22 @@ def test_quantiser_next_to_every_border(dtype):
             # one rounding of the rational value to float32 (float() of a Fraction is the nearest double; where that is
             # halfway between two floats, it is the value itself)
             assert got[0, 0, r].tolist() == [float(np.float32(float(t))) for t in want], r
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("q_size,k_size", [(1e-29, 1e29), (1e-20, 1e30), (1e30, 1e-20), (1e35, 1.0)])
+@pytest.mark.parametrize("unit_keys", [True, False])
+def test_queries_of_any_size(dtype, q_size, k_size, unit_keys):
+    """Queries near both ends of their range, with a scale that keeps the logits ordinary."""
+    g = torch.Generator().manual_seed(88)
+    k = (torch.randn(1, 2, 150, 64, generator=g).clamp(-4, 4) * k_size).to(dtype)
+    v = torch.randn(1, 2, 150, 64, generator=g).to(dtype)
+    c = Cache(88, dtype=dtype, B=1, H=2, D=64, group=32, page=32, ctx=(150,), rows=(k, v))
+    q = (torch.randn(1, 2, 1, 64, generator=g).clamp(-4, 4) * q_size).to(dtype)
+    q[..., 0] = q_size
+    scale = 0.25 / q_size if unit_keys else 0.25 / (q_size * k_size)
+    out, lse = lsh.lsh_cache_attend(q.to(DEV), c.cache, c.table, c.ctx_len, unit_keys=unit_keys, scale=scale,
+                                    out_dtype=torch.float32, **c.form)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    _check_attend(c, q, out, lse, [1], unit_keys=unit_keys, scale=scale)
+    assert _status() == 0
