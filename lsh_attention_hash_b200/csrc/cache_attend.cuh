@@ -49,7 +49,8 @@
 // 17.5 us a call; with two kernels 8.3 us, but another launch and a workspace, 21 to 23 us a call).
 //
 // Measured on the device, one new token, bf16: 8 x 8 heads x 65536 keys of 128 (621 MB) 103 us, 6.0 TB/s, 92 %
-// of the measured copy rate; 8 heads x 1 M keys of 64 (638 MB) 104 us, 6.1 TB/s, 93 %.  Queries a cached head of
+// of the measured copy rate; 8 heads x 1 M keys of 64 (638 MB) 104 us, 6.1 TB/s, 93 %.  (In runs of a second, at the
+// power cap's 1.65 GHz, 114.5 and 118.4 us: instructions weigh there too.)  Queries a cached head of
 // the former: 2 107 us, 4 114 us, 8 161 us, 16 294 us: from 4 on
 // the integer products and the unpacking (198 instructions a tile for one query, set-up and join included) bind.
 // The ring is two stages of 64 tokens a warp and 8 warps an SM at D 128: one stage and 16 warps took as long
