@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import lsh_attention_hash_b200 as lsh
-from tests.test_gpu_cache import DEV, Cache, _status
+from tests.test_gpu_cache import DEV, Cache, _check_attend, _status
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -213,4 +213,19 @@ def test_slices_of_lengths_and_tables():
         graph.replay()
         torch.cuda.synchronize()
         assert same(got, plain())
+    assert _status() == 0
+
+
+@pytest.mark.parametrize("T,ctx,causal,self_mask", [(64, 64, True, True), (257, 300, True, True), (257, 300, False, True),
+                                                   (257, 300, True, False), (1000, 1100, True, True)])
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.float32, 64), (torch.bfloat16, 256)])
+def test_prompt_rows_over_the_cache(T, ctx, causal, self_mask, dtype, D):
+    """Prompts of hundreds of rows, also over earlier tokens, with a shorter prompt in the batch."""
+    c = Cache(93, dtype=dtype, B=2, H=1, D=D, group=64, page=32, ctx=(ctx, ctx // 2))
+    new = [T, T // 3]
+    q = c.rand(2, 1, T, D, dtype=dtype).to(DEV)
+    nl = torch.tensor(new, dtype=torch.int32, device=DEV)
+    out, lse = lsh.lsh_cache_attend(q, c.cache, c.table, c.ctx_len, new_len=nl, causal=causal, self_mask=self_mask,
+                                    **c.form)
+    _check_attend(c, q, out, lse, new, causal=causal, self_mask=self_mask)
     assert _status() == 0
